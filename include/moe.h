@@ -65,7 +65,7 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
 /* Expert activation: ReLU (the walkthrough's STEP 9) or GELU, x * Phi(x) with
  * Phi the standard normal CDF (nanoMoE's MLPExperts, "nanoMoEの深層解剖" slide 32). */
-typedef enum { MOE_ACT_RELU = 1, MOE_ACT_GELU = 2 } moe_activation;
+typedef enum { MOE_ACT_NONE = 0 /* moe_linear only */, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2 } moe_activation;
 
 typedef enum {
     MOE_OK = 0,
@@ -357,6 +357,84 @@ MOE_API moe_status moe_backward(const void *x, moe_dtype dt, const float *W_g, c
                                 const void *H, const void *out_gathered, const void *dy, void *dx, float *dW_g,
                                 float *db_g, float *dW_up, float *dW_down, void *ws, size_t ws_bytes,
                                 void *stream);
+
+/* ---------------------------------------------------------------- around the layer */
+
+/* Layer norm with the residual add ("nanoMoEの深層解剖" slide 4: every block is
+ * attention + normalization, then the MoE layer + normalization):
+ *   h = x + residual, rounded to dt and stored   (h = x when residual is NULL)
+ *   mean = sum h / d,  rstd = 1 / sqrt(sum (h - mean)^2 / d + eps)
+ *   y = (h - mean) * rstd * gamma + beta
+ * The stored (rounded) h is what is normalised, so that moe_layer_norm_backward,
+ * which reads it, differentiates what ran.  Statistics in fp32, y rounded once.
+ *
+ *  x, residual  device [N, d] of dt; residual nullable
+ *  gamma, beta  device [d] fp32, each nullable (1 and 0)
+ *  eps          > 0, finite
+ *  y            device [N, d] of dt out
+ *  sum_out      device [N, d] of dt out: h; required with a residual, else NULL
+ *  mean, rstd   device [N] fp32 out, each nullable
+ * y or sum_out (not both) may be the array x or residual itself.  Any d >= 1;
+ * rows may start at any multiple of the element size. */
+MOE_API moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, const float *gamma,
+                                  const float *beta, float eps, int64_t N, int d, void *y, void *sum_out,
+                                  float *mean, float *rstd, void *stream);
+
+/* Gradients of L = sum dy * y (+ sum dres * h, the skip path's part):
+ *   xh = (h - mean) * rstd,  g = gamma * dy
+ *   dx = dres + rstd * (g - sum(g) / d - xh * sum(g * xh) / d)
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ * dx is the gradient of x and of the residual alike.
+ *  dy, h, dres  device [N, d] of dt; dres nullable
+ *  mean, rstd   device [N] fp32, from moe_layer_norm
+ *  gamma        device [d] fp32, nullable (1)
+ *  dx           device [N, d] of dt out; may be the array dy, h or dres itself
+ *  dgamma, dbeta  device [d] fp32 out (overwritten; zeros for N = 0), each nullable
+ *  ws           scratch of moe_layer_norm_backward_workspace_size() bytes
+ * Deterministic: no atomics decide a sum's order. */
+MOE_API size_t moe_layer_norm_backward_workspace_size(int64_t N, int d, moe_dtype dt);
+MOE_API moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, const float *gamma,
+                                           const float *mean, const float *rstd, const void *dres, int64_t N, int d,
+                                           void *dx, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                                           void *stream);
+
+/* The dense layer beside the experts (a shared expert, or the dense blocks of
+ * a model that uses the layer in some blocks only):
+ *   z = x W^T + b,  y = act(z) + residual
+ *  x         device [N, d_in] of dt
+ *  W         device [d_out, d_in] of dt
+ *  b         device [d_out] fp32, nullable
+ *  activation  MOE_ACT_NONE, MOE_ACT_RELU or MOE_ACT_GELU (erf form)
+ *  residual  device [N, d_out] of dt, nullable; may be the array y itself
+ *  y         device [N, d_out] of dt out, rounded once
+ *  z_out     device [N, d_out] of dt out, nullable: z rounded, for moe_linear_backward
+ *  ws        scratch of moe_linear_workspace_size() bytes (NULL if that is 0)
+ * fp32 accumulation.  A wait of its kernels that runs out is recorded in the
+ * library's own per-device word: moe_check_linear_status(). */
+MOE_API size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt);
+MOE_API moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b, int activation,
+                              const void *residual, int64_t N, int d_in, int d_out, void *y, void *z_out, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* Gradients of L = sum dy * y of moe_linear (the residual's gradient is dy):
+ *   dZ = dy * act'(z),  dx = dZ W,  dW = dZ^T x,  db = sum over rows of dZ
+ *  dy        device [N, d_out] of dt
+ *  x, W      as in the forward
+ *  z         device [N, d_out] of dt: the forward's z_out (NULL for MOE_ACT_NONE)
+ *  dx        device [N, d_in] of dt out, nullable (skipped)
+ *  dW        device [d_out, d_in] of dt out, nullable; overwritten, zeros for N = 0
+ *  db        device [d_out] fp32 out, nullable; overwritten, zeros for N = 0
+ *  ws        scratch of moe_linear_backward_workspace_size() bytes
+ * dZ is rounded to dt before the two products, db sums it unrounded in fp32.
+ * The outputs may not overlap the inputs.  Deterministic. */
+MOE_API size_t moe_linear_backward_workspace_size(int64_t N, int d_in, int d_out, int activation, moe_dtype dt);
+MOE_API moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, const void *W, const void *z,
+                                       int activation, int64_t N, int d_in, int d_out, void *dx, void *dW, float *db,
+                                       void *ws, size_t ws_bytes, void *stream);
+
+/* As moe_check_route_status, for the word of moe_linear and moe_linear_backward
+ * calls on the current device. */
+MOE_API moe_status moe_check_linear_status(void *stream, uint32_t *detail);
 
 /* ---------------------------------------------------------------- fused */
 

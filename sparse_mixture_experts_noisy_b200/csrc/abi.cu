@@ -67,6 +67,15 @@ moe_status check_shape(int64_t N, int d, int E, int k, moe_dtype dt) {
     return MOE_OK;
 }
 
+moe_status check_linear(int64_t N, int d_in, int d_out, moe_dtype dt, int activation) {
+    moe_status st = check_shape(N, d_in, 1, 1, dt);
+    if (st != MOE_OK) return st;
+    if (d_out < 1) return fail(MOE_ERR_INVALID_ARG, "d_out must be >= 1 (got %d)", d_out);
+    if (activation != MOE_ACT_NONE && activation != MOE_ACT_RELU && activation != MOE_ACT_GELU)
+        return fail(MOE_ERR_INVALID_ARG, "activation must be MOE_ACT_NONE, MOE_ACT_RELU or MOE_ACT_GELU");
+    return MOE_OK;
+}
+
 #define REQUIRE_PTR(p, name)                                                                    \
     do {                                                                                        \
         if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s must not be NULL", name);      \
@@ -613,6 +622,132 @@ moe_status moe_load_stats(const int32_t *topk_idx, const float *gates, int64_t N
     cudaError_t e = moe::launch_load_stats(topk_idx, gates, N, E, k, C, load, used, importance, ws,
                                            static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "load statistics launch");
+    return MOE_OK;
+}
+
+moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, const float *gamma, const float *beta,
+                          float eps, int64_t N, int d, void *y, void *sum_out, float *mean, float *rstd,
+                          void *stream) {
+    moe_status st = check_shape(N, d, 1, 1, dt);
+    if (st != MOE_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be > 0 and finite (got %g)", eps);
+    OPTIONAL_PTR(gamma, "gamma");
+    OPTIONAL_PTR(beta, "beta");
+    OPTIONAL_PTR(residual, "residual");
+    OPTIONAL_PTR(mean, "mean");
+    OPTIONAL_PTR(rstd, "rstd");
+    if (N > 0) {
+        REQUIRE_PTR(x, "x");
+        REQUIRE_PTR(y, "y");
+        if (residual != nullptr) REQUIRE_PTR(sum_out, "sum_out");
+    }
+    if (residual == nullptr && sum_out != nullptr)
+        return fail(MOE_ERR_INVALID_ARG, "sum_out must be NULL without a residual (the sum is x)");
+    if (N > 0 && sum_out == y) return fail(MOE_ERR_INVALID_ARG, "y and sum_out must be different arrays");
+    cudaError_t e = moe::launch_norm(x, residual, dt == MOE_BF16 ? 1 : 0, gamma, beta, eps, N, d, y, sum_out, mean,
+                                     rstd, num_sms_current(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "layer norm launch");
+    return MOE_OK;
+}
+
+size_t moe_layer_norm_backward_workspace_size(int64_t N, int d, moe_dtype dt) {
+    if (check_shape(N, d, 1, 1, dt) != MOE_OK) return 0;
+    return moe::norm_bwd_ws_bytes(N, d);
+}
+
+moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, const float *gamma, const float *mean,
+                                   const float *rstd, const void *dres, int64_t N, int d, void *dx, float *dgamma,
+                                   float *dbeta, void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = check_shape(N, d, 1, 1, dt);
+    if (st != MOE_OK) return st;
+    OPTIONAL_PTR(gamma, "gamma");
+    OPTIONAL_PTR(dres, "dres");
+    OPTIONAL_PTR(dgamma, "dgamma");
+    OPTIONAL_PTR(dbeta, "dbeta");
+    if (N > 0) {
+        REQUIRE_PTR(dy, "dy");
+        REQUIRE_PTR(h, "h");
+        REQUIRE_PTR(mean, "mean");
+        REQUIRE_PTR(rstd, "rstd");
+        REQUIRE_PTR(dx, "dx");
+    }
+    const size_t need = moe::norm_bwd_ws_bytes(N, d);
+    if (ws == nullptr || ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "layer norm backward workspace needs %zu bytes (got %zu)", need,
+                    ws == nullptr ? (size_t)0 : ws_bytes);
+    REQUIRE_PTR(ws, "ws");
+    cudaError_t e = moe::launch_norm_bwd(dy, h, dt == MOE_BF16 ? 1 : 0, gamma, mean, rstd, dres, N, d, dx, dgamma,
+                                         dbeta, ws, num_sms_current(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
+    return MOE_OK;
+}
+
+size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt) {
+    if (check_shape(N, d_in, 1, 1, dt) != MOE_OK || d_out < 1) return 0;
+    return moe::linear_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0);
+}
+
+moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b, int activation, const void *residual,
+                      int64_t N, int d_in, int d_out, void *y, void *z_out, void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = check_linear(N, d_in, d_out, dt, activation);
+    if (st != MOE_OK) return st;
+    REQUIRE_PTR(W, "W");
+    OPTIONAL_PTR(b, "b");
+    OPTIONAL_PTR(residual, "residual");
+    OPTIONAL_PTR(z_out, "z_out");
+    if (N > 0) {
+        REQUIRE_PTR(x, "x");
+        REQUIRE_PTR(y, "y");
+        if (z_out == y) return fail(MOE_ERR_INVALID_ARG, "y and z_out must be different arrays");
+    }
+    const size_t need = moe::linear_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0);
+    if (need > 0 && (ws == nullptr || ws_bytes < need))
+        return fail(MOE_ERR_WORKSPACE, "linear workspace needs %zu bytes (got %zu)", need,
+                    ws == nullptr ? (size_t)0 : ws_bytes);
+    OPTIONAL_PTR(ws, "ws");
+    moe::LinearArgs a{x, dt == MOE_BF16 ? 1 : 0, W, b, activation, residual, N, d_in, d_out, y, z_out};
+    cudaError_t e = moe::launch_linear(a, ws, kWaitTimeoutNs, num_sms_current(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "linear launch");
+    return MOE_OK;
+}
+
+size_t moe_linear_backward_workspace_size(int64_t N, int d_in, int d_out, int activation, moe_dtype dt) {
+    if (check_linear(N, d_in, d_out, dt, activation) != MOE_OK) return 0;
+    return moe::linear_bwd_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0, activation);
+}
+
+moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, const void *W, const void *z,
+                               int activation, int64_t N, int d_in, int d_out, void *dx, void *dW, float *db,
+                               void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = check_linear(N, d_in, d_out, dt, activation);
+    if (st != MOE_OK) return st;
+    REQUIRE_PTR(W, "W");
+    OPTIONAL_PTR(dx, "dx");
+    OPTIONAL_PTR(dW, "dW");
+    OPTIONAL_PTR(db, "db");
+    OPTIONAL_PTR(z, "z");
+    if (N > 0) {
+        REQUIRE_PTR(dy, "dy");
+        REQUIRE_PTR(x, "x");
+        if (activation != MOE_ACT_NONE) REQUIRE_PTR(z, "z");
+    }
+    const size_t need = moe::linear_bwd_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0, activation);
+    if (need > 0 && (ws == nullptr || ws_bytes < need))
+        return fail(MOE_ERR_WORKSPACE, "linear backward workspace needs %zu bytes (got %zu)", need,
+                    ws == nullptr ? (size_t)0 : ws_bytes);
+    OPTIONAL_PTR(ws, "ws");
+    moe::LinearBwdArgs a{dy, x, dt == MOE_BF16 ? 1 : 0, W, z, activation, N, d_in, d_out, dx, dW, db};
+    cudaError_t e = moe::launch_linear_bwd(a, ws, kWaitTimeoutNs, num_sms_current(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "linear backward launch");
+    return MOE_OK;
+}
+
+moe_status moe_check_linear_status(void *stream, uint32_t *detail) {
+    uint32_t word = 0;
+    cudaError_t e = moe::linear_status_read_clear(&word, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "linear status read");
+    if (detail) *detail = word;
+    if (word & moe::ST_TIMEOUT) return fail(MOE_ERR_TIMEOUT, "a linear kernel's wait ran out (status 0x%08x)", word);
     return MOE_OK;
 }
 

@@ -173,4 +173,45 @@ cudaError_t launch_tc_bwd_gemms(const BwdArgs &a, const void *dO, void *dZ, void
                                 uint64_t timeout_ns, int num_sms, cudaStream_t s);
 int backward_launches(const BwdArgs &a, bool tensor_cores);
 
+// Layer norm with the residual add, and its backward (norm.cu); pointers as in
+// moe_layer_norm and moe_layer_norm_backward (include/moe.h), dt 1 = bf16.
+size_t norm_bwd_ws_bytes(int64_t N, int d);
+cudaError_t launch_norm(const void *x, const void *residual, int dt, const float *gamma, const float *beta, float eps,
+                        int64_t N, int d, void *y, void *sum_out, float *mean, float *rstd, int num_sms,
+                        cudaStream_t s);
+cudaError_t launch_norm_bwd(const void *dy, const void *h, int dt, const float *gamma, const float *mean,
+                            const float *rstd, const void *dres, int64_t N, int d, void *dx, float *dgamma,
+                            float *dbeta, void *ws, int num_sms, cudaStream_t s);
+
+// Dense layer (linear.cu, linear_tc.cu); pointers as in moe_linear and
+// moe_linear_backward.
+struct LinearArgs {
+    const void *x;
+    int dt;
+    const void *W;
+    const float *b;
+    int act;
+    const void *residual;
+    int64_t M;
+    int d_in, d_out;
+    void *y, *z_out;
+};
+size_t linear_ws_bytes(int64_t M, int d_in, int d_out, int dt);
+cudaError_t launch_linear(const LinearArgs &a, void *ws, uint64_t timeout_ns, int num_sms, cudaStream_t s);
+struct LinearBwdArgs {
+    const void *dy, *x;
+    int dt;
+    const void *W, *z;
+    int act;
+    int64_t M;
+    int d_in, d_out;
+    void *dx, *dW;
+    float *db;
+};
+size_t linear_bwd_ws_bytes(int64_t M, int d_in, int d_out, int dt, int act);
+cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout_ns, int num_sms, cudaStream_t s);
+// Reads and clears (on stream s, then synchronises it) the status word of the
+// dense layer's kernels on the current device.
+cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s);
+
 }  // namespace moe

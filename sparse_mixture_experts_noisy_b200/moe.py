@@ -6,6 +6,7 @@ built, or no CUDA device is present, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -17,7 +18,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
-ACT_RELU, ACT_GELU = 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2  # ACT_NONE: moe_linear only
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_CHECK", 6: "MOE_ERR_TIMEOUT"}
 
@@ -28,6 +29,9 @@ EXPORTS = ("moe_capacity", "moe_gathered_rows", "moe_route", "moe_route_ex", "mo
            "moe_expert_ffn_workspace_size", "moe_expert_ffn", "moe_expert_ffn_ex", "moe_expert_ffn_train",
            "moe_backward_workspace_size", "moe_backward", "moe_combine",
            "moe_load_stats_workspace_size", "moe_load_stats",
+           "moe_layer_norm", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+           "moe_linear_workspace_size", "moe_linear", "moe_linear_backward_workspace_size", "moe_linear_backward",
+           "moe_check_linear_status",
            "moe_workspace_size", "moe_forward", "moe_forward_ex", "moe_forward_launches",
            "moe_set_fused_small_batch", "moe_check_status", "moe_debug_wait_timeout", "moe_num_sms", "moe_last_error")
 
@@ -78,6 +82,14 @@ def load_library(path: str = LIB_PATH):
             "moe_backward": (I, [P, I, P, P, P, I64, I, I, I, I, I64, P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                  P, SZ, P]),
             "moe_combine": (I, [P, P, P, P, P, I, I64, I, I, P, P]),
+            "moe_layer_norm": (I, [P, P, I, P, P, F, I64, I, P, P, P, P, P]),
+            "moe_layer_norm_backward_workspace_size": (SZ, [I64, I, I]),
+            "moe_layer_norm_backward": (I, [P, P, I, P, P, P, P, I64, I, P, P, P, P, SZ, P]),
+            "moe_linear_workspace_size": (SZ, [I64, I, I, I]),
+            "moe_linear": (I, [P, I, P, P, I, P, I64, I, I, P, P, P, SZ, P]),
+            "moe_linear_backward_workspace_size": (SZ, [I64, I, I, I, I]),
+            "moe_linear_backward": (I, [P, P, I, P, P, I, I64, I, I, P, P, P, P, SZ, P]),
+            "moe_check_linear_status": (I, [P, ctypes.POINTER(U32)]),
             "moe_workspace_size": (SZ, [I64, I, I, I, I, D, I]),
             "moe_forward": (I, [P, I, P, P, P, F, I64, I, I, I, I, D, P, P, P, P, P, P, P, P, P, SZ, P]),
             "moe_forward_ex": (I, [P, I, P, P, P, F, I64, I, I, I, I, D, P, P, I, P, P, P, P, P, P, P, P, P, SZ,
@@ -372,6 +384,161 @@ def moe_load_stats(topk_idx, E, cf, gates=None, stream=None):
     _check(L.moe_load_stats(_p(topk_idx), _p(gates), N, E, k, _cf(cf), _p(load), _p(used), _p(imp), _p(ws),
                             ws.numel(), _stream(stream)))
     return dict(load=load, used=used, importance=imp)
+
+
+def _placed(x, stream):
+    """Context in which a call's outputs are allocated and its kernels launched:
+    x's device, and `stream` (which must be of that device) or the current one."""
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        return torch.cuda.stream(stream)
+    if x.device.index != torch.cuda.current_device():
+        return torch.cuda.device(x.device)
+    return contextlib.nullcontext()
+
+
+def _arg(t, name, shape, dtype, device):
+    """t (nullable) as an argument: a contiguous CUDA tensor of this shape, type and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        _cuda(t, name)
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _scratch(ws, device):
+    _cuda(ws, "ws")
+    if ws is not None and (ws.device != device or ws.dtype != torch.uint8):
+        raise ValueError(f"ws must be uint8 on {device}, got {ws.dtype} on {ws.device}")
+
+
+def _rows(x, name):
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(x.shape)}")
+    _cuda(x, name)
+    return x.shape
+
+
+def moe_layer_norm(x, gamma=None, beta=None, eps=1e-5, residual=None, want_stats=False, y=None, sum_out=None,
+                   stream=None):
+    """Layer norm of h = x + residual.  -> (y [N, d], h, mean [N] fp32, rstd [N] fp32).
+    h is x without a residual and the stored sum with one (sum_out, which may
+    be x or residual itself); mean and rstd are None unless want_stats."""
+    L = load_library()
+    N, d = _rows(x, "x")
+    dt, dev = _dt(x), x.device
+    with _placed(x, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if residual is None:
+            h = x
+            if sum_out is not None:
+                raise ValueError("sum_out needs a residual")
+        else:
+            h = sum_out = torch.empty_like(x) if sum_out is None else sum_out
+        mean = rstd = None
+        if want_stats:
+            mean = torch.empty(N, dtype=torch.float32, device=dev)
+            rstd = torch.empty(N, dtype=torch.float32, device=dev)
+        _check(L.moe_layer_norm(x.data_ptr(), _arg(residual, "residual", x.shape, x.dtype, dev), dt,
+                                _arg(gamma, "gamma", (d,), torch.float32, dev),
+                                _arg(beta, "beta", (d,), torch.float32, dev), float(eps), N, d,
+                                _arg(y, "y", x.shape, x.dtype, dev), _arg(sum_out, "sum_out", x.shape, x.dtype, dev),
+                                mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
+                                torch.cuda.current_stream().cuda_stream))
+    return y, h, mean, rstd
+
+
+def moe_layer_norm_backward(dy, h, mean, rstd, gamma=None, dres=None, want_params=True, dx=None, ws=None,
+                            stream=None):
+    """Gradients of moe_layer_norm: h, mean and rstd are its outputs, dres the
+    gradient that reaches h past the norm (nullable).
+    -> dict(dx [N, d] of h's dtype, dgamma [d], dbeta [d] fp32, or None without want_params)."""
+    L = load_library()
+    N, d = _rows(h, "h")
+    dt, dev = _dt(h), h.device
+    with _placed(h, stream):
+        if dx is None:
+            dx = torch.empty_like(h)
+        dg = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
+        db = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
+        if ws is None:
+            ws = torch.empty(L.moe_layer_norm_backward_workspace_size(N, d, dt), dtype=torch.uint8, device=dev)
+        _scratch(ws, dev)
+        if mean is None or rstd is None:
+            raise ValueError("mean and rstd are needed (want_stats=True in the forward)")
+        _check(L.moe_layer_norm_backward(_arg(dy, "dy", h.shape, h.dtype, dev), h.data_ptr(), dt,
+                                         _arg(gamma, "gamma", (d,), torch.float32, dev),
+                                         _arg(mean, "mean", (N,), torch.float32, dev),
+                                         _arg(rstd, "rstd", (N,), torch.float32, dev),
+                                         _arg(dres, "dres", h.shape, h.dtype, dev), N, d,
+                                         _arg(dx, "dx", h.shape, h.dtype, dev),
+                                         dg.data_ptr() if want_params else None,
+                                         db.data_ptr() if want_params else None, ws.data_ptr(), ws.numel(),
+                                         torch.cuda.current_stream().cuda_stream))
+    return dict(dx=dx, dgamma=dg, dbeta=db)
+
+
+def moe_linear(x, W, b=None, act=ACT_NONE, residual=None, keep_z=False, y=None, ws=None, stream=None):
+    """y = act(x W^T + b) + residual.  -> y [N, d_out], or (y, z) with keep_z (z
+    the pre-activations, for moe_linear_backward).  x [N, d_in] and W [d_out,
+    d_in] of one dtype, b [d_out] fp32; residual may be y itself."""
+    L = load_library()
+    N, d_in = _rows(x, "x")
+    d_out = _rows(W, "W")[0]
+    dt, dev = _dt(x), x.device
+    with _placed(x, stream):
+        if y is None:
+            y = torch.empty((N, d_out), dtype=x.dtype, device=dev)
+        z = torch.empty((N, d_out), dtype=x.dtype, device=dev) if keep_z else None
+        need = L.moe_linear_workspace_size(N, d_in, d_out, dt)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _scratch(ws, dev)
+        _check(L.moe_linear(x.data_ptr(), dt, _arg(W, "W", (d_out, d_in), x.dtype, dev),
+                            _arg(b, "b", (d_out,), torch.float32, dev), int(act),
+                            _arg(residual, "residual", (N, d_out), x.dtype, dev), N, d_in, d_out,
+                            _arg(y, "y", (N, d_out), x.dtype, dev), z.data_ptr() if keep_z else None,
+                            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                            torch.cuda.current_stream().cuda_stream))
+    return (y, z) if keep_z else y
+
+
+def moe_linear_backward(dy, x, W, act=ACT_NONE, z=None, want_dx=True, want_dW=True, want_db=True, ws=None,
+                        stream=None):
+    """Gradients of moe_linear (the residual's is dy).  z: the forward's
+    pre-activations (keep_z), needed unless act is ACT_NONE.
+    -> dict(dx [N, d_in] of x's dtype, dW [d_out, d_in] of W's dtype, db [d_out] fp32; None where not wanted)."""
+    L = load_library()
+    N, d_in = _rows(x, "x")
+    d_out = _rows(W, "W")[0]
+    dt, dev = _dt(x), x.device
+    with _placed(x, stream):
+        dx = torch.empty_like(x) if want_dx else None
+        dW = torch.empty_like(W) if want_dW else None
+        db = torch.empty(d_out, dtype=torch.float32, device=dev) if want_db else None
+        need = L.moe_linear_backward_workspace_size(N, d_in, d_out, int(act), dt)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _scratch(ws, dev)
+        _check(L.moe_linear_backward(_arg(dy, "dy", (N, d_out), x.dtype, dev), x.data_ptr(), dt,
+                                     _arg(W, "W", (d_out, d_in), x.dtype, dev),
+                                     _arg(z, "z", (N, d_out), x.dtype, dev), int(act), N, d_in, d_out,
+                                     dx.data_ptr() if want_dx else None, dW.data_ptr() if want_dW else None,
+                                     db.data_ptr() if want_db else None,
+                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                     torch.cuda.current_stream().cuda_stream))
+    return dict(dx=dx, dW=dW, db=db)
+
+
+def check_linear_status(stream=None):
+    """Read/clear the status word of moe_linear and moe_linear_backward calls -> (code, raw word)."""
+    word = ctypes.c_uint32(0)
+    code = load_library().moe_check_linear_status(_stream(stream), ctypes.byref(word))
+    return int(code), int(word.value)
 
 
 def workspace_size(N, d, E, d_ff, k, cf, dtype) -> int:
