@@ -645,14 +645,14 @@ moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, con
         return fail(MOE_ERR_INVALID_ARG, "sum_out must be NULL without a residual (the sum is x)");
     if (N > 0 && sum_out == y) return fail(MOE_ERR_INVALID_ARG, "y and sum_out must be different arrays");
     cudaError_t e = moe::launch_norm(x, residual, dt == MOE_BF16 ? 1 : 0, gamma, beta, eps, N, d, y, sum_out, mean,
-                                     rstd, num_sms_current(), static_cast<cudaStream_t>(stream));
+                                     rstd, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "layer norm launch");
     return MOE_OK;
 }
 
 size_t moe_layer_norm_backward_workspace_size(int64_t N, int d, moe_dtype dt) {
     if (check_shape(N, d, 1, 1, dt) != MOE_OK) return 0;
-    return moe::norm_bwd_ws_bytes(N, d);
+    return moe::norm_bwd_ws_bytes(N, d, dt == MOE_BF16 ? 1 : 0);
 }
 
 moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, const float *gamma, const float *mean,
@@ -671,13 +671,13 @@ moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, 
         REQUIRE_PTR(rstd, "rstd");
         REQUIRE_PTR(dx, "dx");
     }
-    const size_t need = moe::norm_bwd_ws_bytes(N, d);
+    const size_t need = moe::norm_bwd_ws_bytes(N, d, dt == MOE_BF16 ? 1 : 0);
     if (ws == nullptr || ws_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "layer norm backward workspace needs %zu bytes (got %zu)", need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     REQUIRE_PTR(ws, "ws");
     cudaError_t e = moe::launch_norm_bwd(dy, h, dt == MOE_BF16 ? 1 : 0, gamma, mean, rstd, dres, N, d, dx, dgamma,
-                                         dbeta, ws, num_sms_current(), static_cast<cudaStream_t>(stream));
+                                         dbeta, ws, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
     return MOE_OK;
 }

@@ -175,13 +175,12 @@ int backward_launches(const BwdArgs &a, bool tensor_cores);
 
 // Layer norm with the residual add, and its backward (norm.cu); pointers as in
 // moe_layer_norm and moe_layer_norm_backward (include/moe.h), dt 1 = bf16.
-size_t norm_bwd_ws_bytes(int64_t N, int d);
+size_t norm_bwd_ws_bytes(int64_t N, int d, int dt);
 cudaError_t launch_norm(const void *x, const void *residual, int dt, const float *gamma, const float *beta, float eps,
-                        int64_t N, int d, void *y, void *sum_out, float *mean, float *rstd, int num_sms,
-                        cudaStream_t s);
+                        int64_t N, int d, void *y, void *sum_out, float *mean, float *rstd, cudaStream_t s);
 cudaError_t launch_norm_bwd(const void *dy, const void *h, int dt, const float *gamma, const float *mean,
                             const float *rstd, const void *dres, int64_t N, int d, void *dx, float *dgamma,
-                            float *dbeta, void *ws, int num_sms, cudaStream_t s);
+                            float *dbeta, void *ws, cudaStream_t s);
 
 // Dense layer (linear.cu, linear_tc.cu); pointers as in moe_linear and
 // moe_linear_backward.

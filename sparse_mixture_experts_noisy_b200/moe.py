@@ -386,6 +386,9 @@ def moe_load_stats(topk_idx, E, cf, gates=None, stream=None):
     return dict(load=load, used=used, importance=imp)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _placed(x, stream):
     """Context in which a call's outputs are allocated and its kernels launched:
     x's device, and `stream` (which must be of that device) or the current one."""
@@ -393,26 +396,35 @@ def _placed(x, stream):
         if stream.device != x.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
         return torch.cuda.stream(stream)
-    if x.device.index != torch.cuda.current_device():
+    if x.get_device() != torch.cuda.current_device():
         return torch.cuda.device(x.device)
-    return contextlib.nullcontext()
+    return _HERE
 
 
-def _arg(t, name, shape, dtype, device):
-    """t (nullable) as an argument: a contiguous CUDA tensor of this shape, type and device."""
+def _current(index):
+    """The current stream of device `index` as an integer (no Stream object is made)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _arg(t, name, shape, dtype, index):
+    """t (nullable) as an argument: a contiguous tensor of this shape and type on CUDA device `index`."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        _cuda(t, name)
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _cuda(t, name)
+    raise ValueError(f"{name} must be {tuple(shape)} {dtype} on cuda:{index}, "
+                     f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _scratch(ws, device):
+def _scratch(ws, index):
+    """A caller's workspace (nullable) -> (pointer, bytes)."""
+    if ws is None:
+        return None, 0
     _cuda(ws, "ws")
-    if ws is not None and (ws.device != device or ws.dtype != torch.uint8):
-        raise ValueError(f"ws must be uint8 on {device}, got {ws.dtype} on {ws.device}")
+    if ws.get_device() != index or ws.dtype is not torch.uint8:
+        raise ValueError(f"ws must be uint8 on cuda:{index}, got {ws.dtype} on {ws.device}")
+    return ws.data_ptr(), ws.numel()
 
 
 def _rows(x, name):
@@ -429,7 +441,7 @@ def moe_layer_norm(x, gamma=None, beta=None, eps=1e-5, residual=None, want_stats
     be x or residual itself); mean and rstd are None unless want_stats."""
     L = load_library()
     N, d = _rows(x, "x")
-    dt, dev = _dt(x), x.device
+    dt, dev, at = _dt(x), x.device, x.get_device()
     with _placed(x, stream):
         if y is None:
             y = torch.empty_like(x)
@@ -443,12 +455,12 @@ def moe_layer_norm(x, gamma=None, beta=None, eps=1e-5, residual=None, want_stats
         if want_stats:
             mean = torch.empty(N, dtype=torch.float32, device=dev)
             rstd = torch.empty(N, dtype=torch.float32, device=dev)
-        _check(L.moe_layer_norm(x.data_ptr(), _arg(residual, "residual", x.shape, x.dtype, dev), dt,
-                                _arg(gamma, "gamma", (d,), torch.float32, dev),
-                                _arg(beta, "beta", (d,), torch.float32, dev), float(eps), N, d,
-                                _arg(y, "y", x.shape, x.dtype, dev), _arg(sum_out, "sum_out", x.shape, x.dtype, dev),
+        _check(L.moe_layer_norm(x.data_ptr(), _arg(residual, "residual", x.shape, x.dtype, at), dt,
+                                _arg(gamma, "gamma", (d,), torch.float32, at),
+                                _arg(beta, "beta", (d,), torch.float32, at), float(eps), N, d,
+                                _arg(y, "y", x.shape, x.dtype, at), _arg(sum_out, "sum_out", x.shape, x.dtype, at),
                                 mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
-                                torch.cuda.current_stream().cuda_stream))
+                                _current(at)))
     return y, h, mean, rstd
 
 
@@ -459,7 +471,7 @@ def moe_layer_norm_backward(dy, h, mean, rstd, gamma=None, dres=None, want_param
     -> dict(dx [N, d] of h's dtype, dgamma [d], dbeta [d] fp32, or None without want_params)."""
     L = load_library()
     N, d = _rows(h, "h")
-    dt, dev = _dt(h), h.device
+    dt, dev, at = _dt(h), h.device, h.get_device()
     with _placed(h, stream):
         if dx is None:
             dx = torch.empty_like(h)
@@ -467,18 +479,18 @@ def moe_layer_norm_backward(dy, h, mean, rstd, gamma=None, dres=None, want_param
         db = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
         if ws is None:
             ws = torch.empty(L.moe_layer_norm_backward_workspace_size(N, d, dt), dtype=torch.uint8, device=dev)
-        _scratch(ws, dev)
+        wsp, wsn = _scratch(ws, at)
         if mean is None or rstd is None:
             raise ValueError("mean and rstd are needed (want_stats=True in the forward)")
-        _check(L.moe_layer_norm_backward(_arg(dy, "dy", h.shape, h.dtype, dev), h.data_ptr(), dt,
-                                         _arg(gamma, "gamma", (d,), torch.float32, dev),
-                                         _arg(mean, "mean", (N,), torch.float32, dev),
-                                         _arg(rstd, "rstd", (N,), torch.float32, dev),
-                                         _arg(dres, "dres", h.shape, h.dtype, dev), N, d,
-                                         _arg(dx, "dx", h.shape, h.dtype, dev),
+        _check(L.moe_layer_norm_backward(_arg(dy, "dy", h.shape, h.dtype, at), h.data_ptr(), dt,
+                                         _arg(gamma, "gamma", (d,), torch.float32, at),
+                                         _arg(mean, "mean", (N,), torch.float32, at),
+                                         _arg(rstd, "rstd", (N,), torch.float32, at),
+                                         _arg(dres, "dres", h.shape, h.dtype, at), N, d,
+                                         _arg(dx, "dx", h.shape, h.dtype, at),
                                          dg.data_ptr() if want_params else None,
-                                         db.data_ptr() if want_params else None, ws.data_ptr(), ws.numel(),
-                                         torch.cuda.current_stream().cuda_stream))
+                                         db.data_ptr() if want_params else None, wsp, wsn,
+                                         _current(at)))
     return dict(dx=dx, dgamma=dg, dbeta=db)
 
 
@@ -489,7 +501,7 @@ def moe_linear(x, W, b=None, act=ACT_NONE, residual=None, keep_z=False, y=None, 
     L = load_library()
     N, d_in = _rows(x, "x")
     d_out = _rows(W, "W")[0]
-    dt, dev = _dt(x), x.device
+    dt, dev, at = _dt(x), x.device, x.get_device()
     with _placed(x, stream):
         if y is None:
             y = torch.empty((N, d_out), dtype=x.dtype, device=dev)
@@ -497,13 +509,13 @@ def moe_linear(x, W, b=None, act=ACT_NONE, residual=None, keep_z=False, y=None, 
         need = L.moe_linear_workspace_size(N, d_in, d_out, dt)
         if ws is None and need:
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _scratch(ws, dev)
-        _check(L.moe_linear(x.data_ptr(), dt, _arg(W, "W", (d_out, d_in), x.dtype, dev),
-                            _arg(b, "b", (d_out,), torch.float32, dev), int(act),
-                            _arg(residual, "residual", (N, d_out), x.dtype, dev), N, d_in, d_out,
-                            _arg(y, "y", (N, d_out), x.dtype, dev), z.data_ptr() if keep_z else None,
-                            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                            torch.cuda.current_stream().cuda_stream))
+        wsp, wsn = _scratch(ws, at)
+        _check(L.moe_linear(x.data_ptr(), dt, _arg(W, "W", (d_out, d_in), x.dtype, at),
+                            _arg(b, "b", (d_out,), torch.float32, at), int(act),
+                            _arg(residual, "residual", (N, d_out), x.dtype, at), N, d_in, d_out,
+                            _arg(y, "y", (N, d_out), x.dtype, at), z.data_ptr() if keep_z else None,
+                            wsp, wsn,
+                            _current(at)))
     return (y, z) if keep_z else y
 
 
@@ -515,7 +527,7 @@ def moe_linear_backward(dy, x, W, act=ACT_NONE, z=None, want_dx=True, want_dW=Tr
     L = load_library()
     N, d_in = _rows(x, "x")
     d_out = _rows(W, "W")[0]
-    dt, dev = _dt(x), x.device
+    dt, dev, at = _dt(x), x.device, x.get_device()
     with _placed(x, stream):
         dx = torch.empty_like(x) if want_dx else None
         dW = torch.empty_like(W) if want_dW else None
@@ -523,14 +535,14 @@ def moe_linear_backward(dy, x, W, act=ACT_NONE, z=None, want_dx=True, want_dW=Tr
         need = L.moe_linear_backward_workspace_size(N, d_in, d_out, int(act), dt)
         if ws is None and need:
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _scratch(ws, dev)
-        _check(L.moe_linear_backward(_arg(dy, "dy", (N, d_out), x.dtype, dev), x.data_ptr(), dt,
-                                     _arg(W, "W", (d_out, d_in), x.dtype, dev),
-                                     _arg(z, "z", (N, d_out), x.dtype, dev), int(act), N, d_in, d_out,
+        wsp, wsn = _scratch(ws, at)
+        _check(L.moe_linear_backward(_arg(dy, "dy", (N, d_out), x.dtype, at), x.data_ptr(), dt,
+                                     _arg(W, "W", (d_out, d_in), x.dtype, at),
+                                     _arg(z, "z", (N, d_out), x.dtype, at), int(act), N, d_in, d_out,
                                      dx.data_ptr() if want_dx else None, dW.data_ptr() if want_dW else None,
                                      db.data_ptr() if want_db else None,
-                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                     torch.cuda.current_stream().cuda_stream))
+                                     wsp, wsn,
+                                     _current(at)))
     return dict(dx=dx, dW=dW, db=db)
 
 
