@@ -7,20 +7,9 @@
 #include "common.cuh"
 #include "internal.h"
 #include "linear.cuh"
+#include "linear_tc.h"
 
 namespace moe {
-
-// The dense layer's status word on each device (bounded waits of its kernels).
-static __device__ uint32_t g_linear_status;
-
-cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    static const uint32_t zero = 0u;
-    e = cudaMemcpyToSymbolAsync(g_linear_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(s);
-}
 
 namespace {
 
@@ -89,14 +78,56 @@ cudaError_t launch_simt(const SimtArgs &p, cudaStream_t s) {
                       dim3(256), 0, s, p);
 }
 
-// ---------------------------------------------------------------- dZ and db
-// dZ = dy act'(z), rounded to the storage type, and the column sums of the
-// unrounded dZ over a chunk of rows.  A block takes 32 columns, its 8 warps
-// every eighth row of the chunk.
+// ---------------------------------------------------------------- operands for the tensor cores
+// v = p0 + p1 + p2 in bf16 parts (each the rest rounded to bf16; the rests are
+// exact in fp32).  A value above bf16's largest, 3.39e38, has no such parts.
+__device__ __forceinline__ void bf16_parts(float v, __nv_bfloat16 (&p)[3]) {
+    p[0] = __float2bfloat16_rn(v);
+    v -= __bfloat162float(p[0]);
+    p[1] = __float2bfloat16_rn(v);
+    v -= __bfloat162float(p[1]);
+    p[2] = __float2bfloat16_rn(v);
+}
+
+// Writes element (r, c) of an operand: rows of ld elements, `plane` elements
+// from one part to the next (fp32).
+template <typename T>
+__device__ __forceinline__ void put_operand(__nv_bfloat16 *out, int64_t at, int64_t plane, float v) {
+    if constexpr (sizeof(T) == 4) {
+        __nv_bfloat16 p[3];
+        bf16_parts(v, p);
+        out[at] = p[0];
+        out[at + plane] = p[1];
+        out[at + 2 * plane] = p[2];
+    } else {
+        out[at] = __float2bfloat16_rn(v);
+    }
+}
+
+// An array as an operand: rows padded with zeros to ld, fp32 values in parts.
 template <typename T>
 __global__ void __launch_bounds__(256)
-linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int64_t chunk_rows,
-                 T *dz, float *part) {
+linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __nv_bfloat16 *out) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t plane = rows * ld;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < plane; i += step) {
+        const int64_t r = i / ld;
+        const int c = static_cast<int>(i - r * ld);
+        put_operand<T>(out, i, plane, c < cols ? to_f32<T>(in[r * cols + c]) : 0.0f);
+    }
+}
+
+// ---------------------------------------------------------------- dZ and db
+// dZ = dy act'(z), rounded to the storage type and laid out as an operand, and
+// the column sums of the unrounded dZ over a chunk of rows.  A block takes 32
+// columns, its 8 warps every eighth row of the chunk.  dz and part nullable.
+// O: bf16 for an operand (fp32 in parts), T for the CUDA-core products.
+template <typename T, typename O>
+__global__ void __launch_bounds__(256)
+linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
+                 int64_t chunk_rows, O *dz, float *part) {
     __shared__ float red[8][33];
     pdl_trigger();
     pdl_wait();
@@ -105,12 +136,18 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * chunk_rows;
     const int64_t r1 = r0 + chunk_rows < M ? r0 + chunk_rows : M;
     float a = 0.0f;
-    if (col < n)
+    if (col < ld)
         for (int64_t r = r0 + warp; r < r1; r += 8) {
-            float v = to_f32<T>(dy[r * n + col]);
-            if (act != kActNone) v = act_backward(v, to_f32<T>(z[r * n + col]), act);
-            a += v;
-            if (dz != nullptr) dz[r * n + col] = from_f32<T>(v);
+            float v = 0.0f;
+            if (col < n) {
+                v = to_f32<T>(dy[r * n + col]);
+                if (act != kActNone) v = act_backward(v, to_f32<T>(z[r * n + col]), act);
+                a += v;
+            }
+            if (dz != nullptr) {
+                if constexpr (sizeof(O) == sizeof(T)) dz[r * ld + col] = from_f32<T>(v);
+                else put_operand<T>(dz, r * ld + col, M * ld, v);
+            }
         }
     if (part == nullptr) return;
     red[warp][lane] = a;
@@ -146,27 +183,62 @@ int64_t row_chunks(int64_t M) {
 
 }  // namespace
 
-size_t linear_ws_bytes(int64_t, int, int, int) { return 0; }
-
-cudaError_t launch_linear(const LinearArgs &a, void *, uint64_t, int, cudaStream_t s) {
-    if (a.M == 0) return cudaSuccess;
-    SimtArgs p{a.x, a.W, a.d_in, 1, a.d_in, 1, a.M, a.d_out, a.d_in, {a.b, a.act, a.residual, a.y, a.z_out}};
-    return a.dt == 1 ? launch_simt<__nv_bfloat16>(p, s) : launch_simt<float>(p, s);
-}
-
 namespace {
 
-// Byte offsets inside the backward workspace: dZ of the storage type, and the
+int pad8(int n) { return (n + 7) / 8 * 8; }
+
+// bf16 rows of a multiple of 8 elements are operands as they are.
+bool needs_pack(int dt, int cols) { return dt == 0 || cols % 8 != 0; }
+
+size_t operand_bytes(int64_t rows, int cols, int dt) {
+    return align_up(static_cast<size_t>(rows) * pad8(cols) * 2 * (dt == 0 ? 3 : 1), 256);
+}
+
+// `in` as an operand at `out` (scratch) if it is not one already.
+template <typename T>
+cudaError_t pack(const void *&in, int64_t rows, int cols, void *out, cudaStream_t s) {
+    if (!needs_pack(sizeof(T) == 2 ? 1 : 0, cols)) return cudaSuccess;
+    const int64_t n = rows * pad8(cols), blocks = (n + 1023) / 1024;
+    cudaError_t e = launch_pdl(linear_pack_kernel<T>, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)),
+                               dim3(256), 0, s, static_cast<const T *>(in), rows, cols, pad8(cols),
+                               static_cast<__nv_bfloat16 *>(out));
+    in = out;
+    return e;
+}
+
+// Products too small for the tensor-core kernels' setup run on CUDA cores.
+bool use_simt(int64_t M, int d_in, int d_out) { return M * d_in * static_cast<int64_t>(d_out) <= (1 << 18); }
+
+struct FwdScratch {
+    size_t x, W, total;
+};
+FwdScratch fwd_scratch(int64_t M, int d_in, int d_out, int dt) {
+    FwdScratch L{};
+    if (M == 0 || use_simt(M, d_in, d_out) || !needs_pack(dt, d_in)) return L;
+    L.W = operand_bytes(M, d_in, dt);
+    L.total = L.W + operand_bytes(d_out, d_in, dt);
+    return L;
+}
+
+// Byte offsets inside the backward workspace: dZ, x and W as operands, and the
 // row chunks' partial sums of db.
 struct BwdScratch {
-    size_t dz, part, total;
+    size_t dz, x, W, part, total;
 };
-
-BwdScratch bwd_scratch(int64_t M, int d_out, int dt, int act) {
+BwdScratch bwd_scratch(int64_t M, int d_in, int d_out, int dt, int act) {
     BwdScratch L{};
     size_t o = 0;
+    const bool simt = use_simt(M, d_in, d_out);
     L.dz = o;
-    if (act != kActNone) o += align_up(static_cast<size_t>(M) * d_out * (dt == 1 ? 2 : 4), 256);
+    if (simt) {
+        if (act != kActNone) o += align_up(static_cast<size_t>(M) * d_out * 4, 256);
+    } else if (act != kActNone || needs_pack(dt, d_out)) {
+        o += operand_bytes(M, d_out, dt);
+    }
+    L.x = o;
+    if (!simt && needs_pack(dt, d_in)) o += operand_bytes(M, d_in, dt);
+    L.W = o;
+    if (!simt && needs_pack(dt, d_in)) o += operand_bytes(d_out, d_in, dt);
     L.part = o;
     o += align_up(static_cast<size_t>(row_chunks(M)) * d_out * sizeof(float), 256);
     L.total = o;
@@ -175,46 +247,94 @@ BwdScratch bwd_scratch(int64_t M, int d_out, int dt, int act) {
 
 }  // namespace
 
-size_t linear_bwd_ws_bytes(int64_t M, int, int d_out, int dt, int act) { return bwd_scratch(M, d_out, dt, act).total; }
+size_t linear_ws_bytes(int64_t M, int d_in, int d_out, int dt) { return fwd_scratch(M, d_in, d_out, dt).total; }
 
-cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t, int, cudaStream_t s) {
+cudaError_t launch_linear(const LinearArgs &a, void *ws, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
+    if (a.M == 0) return cudaSuccess;
+    const LinearEpi epi{a.b, a.act, a.residual, a.y, a.z_out};
+    auto go = [&](auto tag) {
+        using T = decltype(tag);
+        if (use_simt(a.M, a.d_in, a.d_out)) {
+            SimtArgs p{a.x, a.W, a.d_in, 1, a.d_in, 1, a.M, a.d_out, a.d_in, epi};
+            return launch_simt<T>(p, s);
+        }
+        const FwdScratch L = fwd_scratch(a.M, a.d_in, a.d_out, a.dt);
+        uint8_t *w = static_cast<uint8_t *>(ws);
+        const void *x = a.x, *W = a.W;
+        cudaError_t e = pack<T>(x, a.M, a.d_in, w + L.x, s);
+        if (e == cudaSuccess) e = pack<T>(W, a.d_out, a.d_in, w + L.W, s);
+        if (e != cudaSuccess) return e;
+        const TcProduct t{W, x, a.M, a.d_out, a.d_in, false, false, epi};
+        return launch_tc_products(&t, 1, sizeof(T) == 4, true, timeout_ns, num_sms, s);
+    };
+    return a.dt == 1 ? go(__nv_bfloat16{}) : go(float{});
+}
+
+size_t linear_bwd_ws_bytes(int64_t M, int d_in, int d_out, int dt, int act) {
+    return bwd_scratch(M, d_in, d_out, dt, act).total;
+}
+
+cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
     const size_t es = a.dt == 1 ? 2 : 4;
-    cudaError_t e = cudaSuccess;
     if (a.M == 0) {
+        cudaError_t e = cudaSuccess;
         if (a.dW != nullptr) e = cudaMemsetAsync(a.dW, 0, es * static_cast<size_t>(a.d_in) * a.d_out, s);
         if (e == cudaSuccess && a.db != nullptr) e = cudaMemsetAsync(a.db, 0, sizeof(float) * static_cast<size_t>(a.d_out), s);
         return e;
     }
-    const BwdScratch L = bwd_scratch(a.M, a.d_out, a.dt, a.act);
+    const BwdScratch L = bwd_scratch(a.M, a.d_in, a.d_out, a.dt, a.act);
     uint8_t *w = static_cast<uint8_t *>(ws);
     auto go = [&](auto tag) {
         using T = decltype(tag);
         cudaError_t e = cudaSuccess;
-        const bool need_dz = a.act != kActNone && (a.dx != nullptr || a.dW != nullptr);
-        T *dzw = need_dz ? reinterpret_cast<T *>(w + L.dz) : nullptr;
+        const bool simt = use_simt(a.M, a.d_in, a.d_out);
+        const bool products = a.dx != nullptr || a.dW != nullptr;
+        const bool make_dz = products && (a.act != kActNone || (!simt && needs_pack(a.dt, a.d_out)));
         float *part = a.db != nullptr ? reinterpret_cast<float *>(w + L.part) : nullptr;
-        const unsigned cols = static_cast<unsigned>((static_cast<int64_t>(a.d_out) + 31) / 32);
         const int64_t chunks = row_chunks(a.M);
-        if (dzw != nullptr || part != nullptr) {
-            e = launch_pdl(linear_dz_kernel<T>, dim3(cols, static_cast<unsigned>(chunks)), dim3(256), 0, s,
-                           static_cast<const T *>(a.dy), static_cast<const T *>(a.z), a.act, a.M, a.d_out,
-                           (a.M + chunks - 1) / chunks, dzw, part);
+        const void *dz = make_dz ? static_cast<const void *>(w + L.dz) : a.dy;
+        if (make_dz || part != nullptr) {
+            // on CUDA cores dZ stays in the storage type; otherwise it is laid out as an operand
+            const int ld = simt ? a.d_out : pad8(a.d_out);
+            const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(ld) + 31) / 32), static_cast<unsigned>(chunks));
+            if (simt)
+                e = launch_pdl(linear_dz_kernel<T, T>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
+                               static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
+                               make_dz ? reinterpret_cast<T *>(w + L.dz) : nullptr, part);
+            else
+                e = launch_pdl(linear_dz_kernel<T, __nv_bfloat16>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
+                               static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
+                               make_dz ? reinterpret_cast<__nv_bfloat16 *>(w + L.dz) : nullptr, part);
             if (e != cudaSuccess) return e;
         }
         if (part != nullptr) {
-            e = launch_pdl(linear_db_kernel, dim3(cols), dim3(256), 0, s, part, chunks, a.d_out, a.db);
+            e = launch_pdl(linear_db_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(a.d_out) + 31) / 32)),
+                           dim3(256), 0, s, part, chunks, a.d_out, a.db);
             if (e != cudaSuccess) return e;
         }
-        const void *dz = a.act == kActNone ? a.dy : static_cast<const void *>(dzw);
-        if (a.dx != nullptr) {
-            SimtArgs p{dz, a.W, a.d_out, 1, 1, a.d_in, a.M, a.d_in, a.d_out, {nullptr, kActNone, nullptr, a.dx, nullptr}};
-            if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
+        if (!products) return e;
+        if (simt) {
+            if (a.dx != nullptr) {
+                SimtArgs p{dz, a.W, a.d_out, 1, 1, a.d_in, a.M, a.d_in, a.d_out, {nullptr, kActNone, nullptr, a.dx, nullptr}};
+                if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
+            }
+            if (a.dW != nullptr) {
+                SimtArgs p{dz, a.x, 1, a.d_out, 1, a.d_in, a.d_out, a.d_in, a.M, {nullptr, kActNone, nullptr, a.dW, nullptr}};
+                if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
+            }
+            return e;
         }
-        if (a.dW != nullptr) {
-            SimtArgs p{dz, a.x, 1, a.d_out, 1, a.d_in, a.d_out, a.d_in, a.M, {nullptr, kActNone, nullptr, a.dW, nullptr}};
-            if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
-        }
-        return e;
+        const void *x = a.x, *W = a.W;
+        if (a.dW != nullptr) e = pack<T>(x, a.M, a.d_in, w + L.x, s);
+        if (e == cudaSuccess && a.dx != nullptr) e = pack<T>(W, a.d_out, a.d_in, w + L.W, s);
+        if (e != cudaSuccess) return e;
+        TcProduct t[2];
+        int n = 0;
+        if (a.dW != nullptr)
+            t[n++] = TcProduct{x, dz, a.d_out, a.d_in, static_cast<int>(a.M), true, true, {nullptr, kActNone, nullptr, a.dW, nullptr}};
+        if (a.dx != nullptr)
+            t[n++] = TcProduct{W, dz, a.M, a.d_in, a.d_out, true, false, {nullptr, kActNone, nullptr, a.dx, nullptr}};
+        return launch_tc_products(t, n, sizeof(T) == 4, false, timeout_ns, num_sms, s);
     };
     return a.dt == 1 ? go(__nv_bfloat16{}) : go(float{});
 }

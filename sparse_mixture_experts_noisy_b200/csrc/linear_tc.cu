@@ -1,0 +1,790 @@
+// The dense layer's products on the fifth-generation tensor cores.
+//
+//   D[m][n] = sum_k Q(m, k) P(n, k)
+// with n the contiguous index of the output row.  P is the MMA's A operand and Q
+// its B operand, so a lane of tensor memory holds one n and a column one m: a
+// warp stores 32 neighbouring elements of an output row whatever its width and
+// alignment, and the bias is one value per lane.
+//   forward   D = y  [M][d_out]     P = W  [d_out][d_in]          Q = x  [M][d_in]       k = d_in
+//   dx        D = dx [M][d_in]      P = W  [k = d_out][d_in] (MN) Q = dZ [M][d_out]      k = d_out
+//   dW        D = dW [d_out][d_in]  P = x  [k = M][d_in]     (MN) Q = dZ [k = M][d_out] (MN)
+// "(MN)": the operand is stored with k as its rows; the MMA reads such a tile
+// MN-major, so nothing is transposed in memory.  TMA fills what lies outside an
+// array with zeros, so no size has to be a multiple of a tile.
+//
+// fp32 storage runs on the bf16 tensor cores: each value is split into three
+// bf16 parts, v = v0 + v1 + v2 (8 significant bits each), stored as three
+// planes, and the six products of parts p, q with p + q <= 2 are summed; the
+// three that are left out are below 2^-24 of the product.  Each product of two
+// parts is exact in fp32.  The tensor core truncates when it adds to its
+// accumulator, an error that grows with the number of additions, so K is cut
+// into pieces of kPieceKb blocks: each starts from zero, takes the five small
+// products before the large one, and is added to the others in registers.
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+#include "linear.cuh"
+#include "linear_tc.h"
+#include "tmap.h"
+
+namespace moe {
+
+// The dense layer's status word on each device (bounded waits of its kernels).
+static __device__ uint32_t g_linear_status;
+
+cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
+    if (e != cudaSuccess) return e;
+    static const uint32_t zero = 0u;
+    e = cudaMemcpyToSymbolAsync(g_linear_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(s);
+}
+
+namespace {
+
+constexpr int kBK = 64;        // K elements per stage: 128 bytes, one swizzle row
+constexpr int kPieceKb = 16;   // K blocks per piece of an fp32 product
+constexpr int kTerms = 6;      // products of parts, the largest last
+
+// Plane of P and of Q for term t: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
+__device__ __forceinline__ int term_p(int t) { return t == 1 ? 2 : (t == 2 || t == 4) ? 1 : 0; }
+__device__ __forceinline__ int term_q(int t) { return t == 0 ? 2 : (t == 2 || t == 3) ? 1 : 0; }
+
+struct ProdArgs {
+    int64_t M;      // rows of D
+    int Nn, kb;     // columns of D, K blocks
+    int p_mn, q_mn; // operand stored with k as its rows
+    LinearEpi epi;
+};
+
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > timeout_ns) return false;
+    return true;
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Stores up to CN accumulated columns (rows m0.. of D, `cols` of them valid) of
+// this lane's n.  FULL: bias, activation, residual and z as the epilogue says;
+// otherwise the value alone.
+template <typename T, bool FULL, int CN>
+__device__ __forceinline__ void store_cols(const LinearEpi &e, const float *v, int64_t m0, int n, int ld, int cols,
+                                           float bias) {
+    int64_t at = m0 * ld + n;
+    T *out = static_cast<T *>(e.out);
+    if constexpr (!FULL) {
+#pragma unroll
+        for (int i = 0; i < CN; ++i, at += ld)
+            if (i < cols) out[at] = from_f32<T>(v[i]);
+    } else {
+        float res[CN];
+        if (e.residual != nullptr) {
+            const T *p = static_cast<const T *>(e.residual) + at;
+#pragma unroll
+            for (int i = 0; i < CN; ++i) {
+                res[i] = i < cols ? to_f32<T>(*p) : 0.0f;
+                p += ld;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CN; ++i, at += ld) {
+            if (i < cols) {
+                float u = v[i] + bias;
+                if (e.z_out != nullptr) static_cast<T *>(e.z_out)[at] = from_f32<T>(u);
+                u = act_value(u, e.act);
+                if (e.residual != nullptr) u += res[i];
+                out[at] = from_f32<T>(u);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// A pair of CTAs (tcgen05 cta_group::2) computes 256 x 256 tiles of D: CTA r
+// loads P rows [n0 + 128 r, +128) and Q rows [m0 + 128 r, +128) per K block, the
+// leader's MMA reads both, and each CTA's tensor memory gets its 128 n of all
+// 256 m.  Persistent, one pair per two SMs; two accumulators, so the epilogue of
+// one tile (or piece) overlaps the MMAs of the next.  Warp 0: TMA; warp 1: MMA;
+// warps 2-9: epilogue, two groups of four, each half of the m.
+//
+// One launch runs one product or two (dW, then dx).  A unit is a tile of a
+// product; the first product's units are dealt in turn, and the second's start
+// with the pairs that got one fewer of the first's, as many as fit into the time
+// the others still need, before they are dealt to all.
+constexpr int kPairThreads = 320;
+constexpr int kPairStages = 6;
+constexpr int kGroupM = 8;  // m tiles that share a sweep over n: their Q rows stay in L2
+
+struct PairArgs {
+    ProdArgs p[2];
+    int units[2];
+    int late, early;  // second product: pairs [0, late) start late; the others do `early` units first
+    uint64_t timeout_ns;
+};
+
+struct PairUnit {
+    int prob, n0;
+    int64_t m0;
+};
+
+__device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npairs, int i, PairUnit &t) {
+    const int n1 = pair < a.units[0] ? (a.units[0] - pair + npairs - 1) / npairs : 0;
+    int u;
+    if (i < n1) {
+        t.prob = 0;
+        u = pair + i * npairs;
+    } else {
+        t.prob = 1;
+        i -= n1;
+        const int head = a.early * (npairs - a.late);
+        if (pair >= a.late && i < a.early) {
+            u = (pair - a.late) + i * (npairs - a.late);
+        } else {
+            u = head + pair + (pair >= a.late ? i - a.early : i) * npairs;
+        }
+        if (u >= a.units[1]) return false;
+    }
+    const ProdArgs &p = a.p[t.prob];
+    const int mt = static_cast<int>((p.M + 255) / 256), nt = (p.Nn + 255) / 256;
+    const int sweep = kGroupM * nt;
+    const int grp = u / sweep, rem = u - grp * sweep;
+    const int rows = mt - grp * kGroupM < kGroupM ? mt - grp * kGroupM : kGroupM;
+    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * 256;
+    t.n0 = rem / rows * 256;
+    return true;
+}
+
+template <typename T, bool FULL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constant__ CUtensorMap tq0,
+                   const __grid_constant__ CUtensorMap tp1, const __grid_constant__ CUtensorMap tq1,
+                   const __grid_constant__ PairArgs args) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr int TERMS = SPLIT ? kTerms : 1;
+    constexpr int STAGES = kPairStages;
+    constexpr uint32_t A_BYTES = 128 * kBK * 2, STAGE_BYTES = 2 * A_BYTES;
+
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
+    __shared__ uint32_t tmem_holder;
+    __shared__ uint32_t cta_status;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    uint32_t *status = &cta_status;
+    const uint64_t tmo = args.timeout_ns;
+    const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
+    const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
+    const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
+    const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]);
+    const uint32_t full0_lead = map_to_cta(full0, 0), tempty0_lead = map_to_cta(tempty0, 0);
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(tfull0, 1);
+        mbar_init(tfull0 + 8, 1);
+        mbar_init(tempty0, 16);  // 8 epilogue warps in each CTA
+        mbar_init(tempty0 + 8, 16);
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        cta_status = 0u;
+        tma_prefetch_desc(&tp0);
+        tma_prefetch_desc(&tq0);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_holder;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint64_t pol = policy_evict_normal();
+            PairUnit t;
+            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+                const ProdArgs &p = args.p[t.prob];
+                const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
+                const int nr = t.n0 + static_cast<int>(rank) * 128;
+                const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * 128;
+                const int piece = SPLIT ? kPieceKb : p.kb;
+                for (int k0 = 0; k0 < p.kb && ok; k0 += piece) {
+                    const int k1 = k0 + piece < p.kb ? k0 + piece : p.kb;
+                    for (int x = 0; x < TERMS && ok; ++x) {
+                        const int zp = SPLIT ? term_p(x) : 0, zq = SPLIT ? term_q(x) : 0;
+                        for (int kb = k0; kb < k1; ++kb) {
+                            if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 61)) {
+                                ok = false;
+                                break;
+                            }
+                            if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+                            const uint32_t fb = full0_lead + 8 * stage;
+                            const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                            const int kx = kb * kBK;
+                            if (p.p_mn) {
+                                tma_load_3d_pair(sa, tp, fb, nr, kx, zp, pol);
+                                tma_load_3d_pair(sa + 8192u, tp, fb, nr + 64, kx, zp, pol);
+                            } else {
+                                tma_load_3d_pair(sa, tp, fb, kx, nr, zp, pol);
+                            }
+                            if (p.q_mn) {
+                                tma_load_3d_pair(sa + A_BYTES, tq, fb, mr, kx, zq, pol);
+                                tma_load_3d_pair(sa + A_BYTES + 8192u, tq, fb, mr + 64, kx, zq, pol);
+                            } else {
+                                tma_load_3d_pair(sa + A_BYTES, tq, fb, kx, mr, zq, pol);
+                            }
+                            ++issued;
+                            if (++stage == STAGES) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                    }
+                }
+            }
+            if (!ok && leader) {
+                // the pair's copies of the stages armed here land before exit
+                int st = stage;
+                uint32_t ph = phase;
+                for (int i = 0; i < STAGES && i < issued; ++i) {
+                    if (st == 0) {
+                        st = STAGES - 1;
+                        ph ^= 1u;
+                    } else {
+                        --st;
+                    }
+                    wait_drain(full0 + 8 * st, ph, tmo);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            PairUnit t;
+            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+                const ProdArgs &p = args.p[t.prob];
+                const bool pm = p.p_mn != 0, qm = p.q_mn != 0;
+                const uint32_t idesc = idesc_bf16_f32(256, 256) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
+                // K-major: the next 16 of K are 32 bytes on in the swizzled row;
+                // MN-major: 16 rows of 128 bytes on
+                const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
+                const int piece = SPLIT ? kPieceKb : p.kb;
+                for (int k0 = 0; k0 < p.kb && ok; k0 += piece) {
+                    const int n = (k0 + piece < p.kb ? piece : p.kb - k0) * TERMS;
+                    const int acc = local & 1;
+                    if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 62)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+                    for (int k = 0; k < n; ++k) {
+                        if (!mbar_wait_bounded(full0 + 8 * stage, phase, status, tmo, 63)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                        const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
+                        const uint64_t bd = qm ? smem_desc_mn_sw128(sa + A_BYTES, 8192u, 1024u)
+                                               : smem_desc_sw128(sa + A_BYTES);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            umma_bf16_pair(d_tmem, ad + astep * kk, bd + bstep * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                        any = true;
+                        umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair_mc(tfull0 + 8 * acc, 0x3);
+                    ++local;
+                }
+            }
+            if (!ok && any) {
+                umma_commit_pair(drain);
+                wait_drain(drain, 0, tmo);
+            }
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        int local = 0;
+        bool ok = true;
+        PairUnit t;
+        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+            const ProdArgs &p = args.p[t.prob];
+            const int n = t.n0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+            const int64_t m0 = t.m0 + half * 128;
+            const int64_t left = p.M - m0;
+            const int rows = left < 128 ? static_cast<int>(left > 0 ? left : 0) : 128;
+            const float bias = (FULL && p.epi.bias != nullptr && n < p.Nn) ? p.epi.bias[n] : 0.0f;
+            float sum[SPLIT ? 128 : 1];
+            const int pieces = SPLIT ? (p.kb + kPieceKb - 1) / kPieceKb : 1;
+            for (int pc = 0; pc < pieces; ++pc) {
+                const int acc = local & 1;
+                if (!mbar_wait_warp(tfull0 + 8 * acc, (local >> 1) & 1, status, tmo, 64)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(acc * 256 + half * 128);
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(taddr + c * 16, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c * 16 + j] = pc == 0 ? __uint_as_float(r[j]) : sum[c * 16 + j] + __uint_as_float(r[j]);
+                    }
+                } else {
+                    for (int c = 0; c * 32 < rows; ++c) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(taddr + c * 32, r);
+                        tmem_wait_ld();
+                        if (n < p.Nn)
+                            store_cols<T, FULL, 32>(p.epi, reinterpret_cast<const float *>(r), m0 + c * 32, n, p.Nn,
+                                                    rows - c * 32, bias);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(tempty0 + 8 * acc);
+                    else mbar_arrive_cluster(tempty0_lead + 8 * acc);
+                }
+                ++local;
+            }
+            if constexpr (SPLIT) {
+                if (ok && n < p.Nn) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (c * 8 < rows)
+                            store_cols<T, FULL, 8>(p.epi, sum + c * 8, m0 + c * 8, n, p.Nn, rows - c * 8, bias);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0) publish_status(&g_linear_status, cta_status);
+    cluster_sync();  // the pair's MMAs and remote arrivals are done before TMEM goes
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- one CTA, K split over a cluster
+// For products with few tiles.  A cluster of S CTAs computes a 128 (n) x BN (m)
+// tile of D, CTA r its share of the K blocks; each leaves its sums in shared
+// memory, and after a cluster barrier CTA r adds the S parts of its share of the
+// columns in order (through distributed shared memory) and stores them.  Small
+// batches stream W this way: BN is the batch rounded up to 16, 32, 64 or 128.
+// Two CTAs fit an SM, so one's start and end overlap the other's copies.
+constexpr int kSplitThreads = 192;
+constexpr int kSplitSmem = 108 * 1024;
+
+template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constant__ CUtensorMap tq, const ProdArgs p,
+                    const int S, const int stages, const uint64_t tmo) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr int TERMS = SPLIT ? kTerms : 1;
+    constexpr int COLS = BN < 32 ? 32 : BN;  // tensor-memory columns of one accumulator
+    constexpr uint32_t TMEM_COLS = 2 * COLS;
+    constexpr uint32_t A_BYTES = 128 * kBK * 2;
+    constexpr int kMaxStages = 6;
+    const uint32_t b_bytes = split_b_bytes<BN>(p.q_mn != 0);
+    const uint32_t stage_bytes = A_BYTES + b_bytes;
+
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+    __shared__ uint32_t tmem_holder;
+    __shared__ uint32_t cta_status;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    uint32_t *status = &cta_status;
+    const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
+    const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kMaxStages]);
+    const uint32_t tfull0 = smem_u32(&bars[2 * kMaxStages]), tempty0 = smem_u32(&bars[2 * kMaxStages + 2]);
+    const uint32_t drain = smem_u32(&bars[2 * kMaxStages + 4]);
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(tfull0, 1);
+        mbar_init(tfull0 + 8, 1);
+        mbar_init(tempty0, 4);
+        mbar_init(tempty0 + 8, 4);
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        cta_status = 0u;
+        tma_prefetch_desc(&tp);
+        tma_prefetch_desc(&tq);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_holder), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_holder;
+    pdl_wait();
+
+    const int nt = (p.Nn + 127) / 128;
+    const int64_t tile = blockIdx.x / static_cast<unsigned>(S);
+    const int n0 = static_cast<int>(tile % nt) * 128;
+    const int64_t m0 = tile / nt * BN;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S);
+    const int piece = SPLIT ? kPieceKb : kb1 - kb0;
+
+    float sum[BN];
+    bool good = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int k0 = kb0; k0 < kb1 && ok; k0 += piece) {
+                const int k1 = k0 + piece < kb1 ? k0 + piece : kb1;
+                for (int x = 0; x < TERMS && ok; ++x) {
+                    const int zp = SPLIT ? term_p(x) : 0, zq = SPLIT ? term_q(x) : 0;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 71)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
+                        mbar_arrive_expect_tx(fb, stage_bytes);
+                        const int kx = kb * kBK, mr = static_cast<int>(m0);
+                        if (p.p_mn) {
+                            tma_load_3d(sa, &tp, fb, n0, kx, zp);
+                            tma_load_3d(sa + 8192u, &tp, fb, n0 + 64, kx, zp);
+                        } else {
+                            tma_load_3d(sa, &tp, fb, kx, n0, zp);
+                        }
+                        if (p.q_mn) {
+                            tma_load_3d(sa + A_BYTES, &tq, fb, mr, kx, zq);
+                            if constexpr (BN == 128) tma_load_3d(sa + A_BYTES + 8192u, &tq, fb, mr + 64, kx, zq);
+                        } else {
+                            tma_load_3d(sa + A_BYTES, &tq, fb, kx, mr, zq);
+                        }
+                        ++issued;
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                int st = stage;
+                uint32_t ph = phase;
+                for (int i = 0; i < stages && i < issued; ++i) {
+                    if (st == 0) {
+                        st = stages - 1;
+                        ph ^= 1u;
+                    } else {
+                        --st;
+                    }
+                    wait_drain(full0 + 8 * st, ph, tmo);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            const bool pm = p.p_mn != 0, qm = p.q_mn != 0;
+            const uint32_t idesc = idesc_bf16_f32(128, BN) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
+            const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
+            for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++local) {
+                const int n = (k0 + piece < kb1 ? piece : kb1 - k0) * TERMS;
+                const int acc = local & 1;
+                if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 72)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * COLS);
+                for (int k = 0; k < n; ++k) {
+                    if (!mbar_wait_bounded(full0 + 8 * stage, phase, status, tmo, 73)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_base + stage * stage_bytes;
+                    const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
+                    const uint64_t bd = qm ? smem_desc_mn_sw128(sa + A_BYTES, 8192u, 1024u) : smem_desc_sw128(sa + A_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16(d_tmem, ad + astep * kk, bd + bstep * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                    any = true;
+                    umma_commit(empty0 + 8 * stage);
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) umma_commit(tfull0 + 8 * acc);
+            }
+            if (!ok && any) {
+                umma_commit(drain);
+                wait_drain(drain, 0, tmo);
+            }
+        }
+    } else {
+        const int q = warp & 3;
+        int local = 0;
+        for (int k0 = kb0; k0 < kb1; k0 += piece, ++local) {
+            const int acc = local & 1;
+            if (!mbar_wait_warp(tfull0 + 8 * acc, (local >> 1) & 1, status, tmo, 74)) {
+                good = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * COLS);
+#pragma unroll
+            for (int c = 0; c < BN / 16; ++c) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(taddr + c * 16, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    sum[c * 16 + j] = local == 0 ? __uint_as_float(r[j]) : sum[c * 16 + j] + __uint_as_float(r[j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
+        }
+        if (S > 1 && good) {
+            // the ring is idle: every copy has landed and every MMA has read it
+            float *part = reinterpret_cast<float *>(dyn_smem + (smem_base - smem_u32(dyn_smem)));
+#pragma unroll
+            for (int j = 0; j < BN; ++j) part[j * 128 + q * 32 + lane] = sum[j];
+        }
+    }
+    const int64_t left = p.M - m0;
+    const int rows = left < BN ? static_cast<int>(left) : BN;
+    const int lane_n = (warp & 3) * 32 + lane, n = n0 + lane_n;
+    if (S > 1) {
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+        if (warp >= 2 && n < p.Nn) {
+            const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
+            for (int j = rank; j < rows; j += S) {
+                float v = 0.0f;
+                for (int c = 0; c < S; ++c) {
+                    float u;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u)
+                                 : "r"(map_to_cta(smem_base + static_cast<uint32_t>(j * 128 + lane_n) * 4u, c))
+                                 : "memory");
+                    v += u;
+                }
+                const int64_t at = (m0 + j) * p.Nn + n;
+                v += bias;
+                if (p.epi.z_out != nullptr) static_cast<T *>(p.epi.z_out)[at] = from_f32<T>(v);
+                v = act_value(v, p.epi.act);
+                if (p.epi.residual != nullptr) v += to_f32<T>(static_cast<const T *>(p.epi.residual)[at]);
+                static_cast<T *>(p.epi.out)[at] = from_f32<T>(v);
+            }
+        }
+    } else if (warp >= 2 && good && n < p.Nn) {
+        const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < BN / 8; ++c)
+            if (c * 8 < rows) store_cols<T, true, 8>(p.epi, sum + c * 8, m0 + c * 8, n, p.Nn, rows - c * 8, bias);
+    }
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0) publish_status(&g_linear_status, cta_status);
+    if (S > 1) cluster_sync();  // no CTA leaves while another reads its sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+ProdArgs prod_args(const TcProduct &t) {
+    return ProdArgs{t.M, t.Nn, (t.K + kBK - 1) / kBK, t.p_mn ? 1 : 0, t.q_mn ? 1 : 0, t.epi};
+}
+
+// Tensor maps of both operands: `planes` planes of [k][row] or [row][k], each
+// row `ld` elements (a multiple of 8).
+bool operand_map(CUtensorMap *m, const void *base, int planes, int64_t rows, int K, bool mn, int box) {
+    const int64_t inner = mn ? (rows + 7) / 8 * 8 : (static_cast<int64_t>(K) + 7) / 8 * 8;
+    const int64_t outer = mn ? K : rows;
+    return make_tmap_bf16_3d(m, base, planes, static_cast<int>(outer), static_cast<int>(inner), mn ? 64 : box);
+}
+
+int pair_units(const TcProduct &t) { return static_cast<int>((t.M + 255) / 256) * ((t.Nn + 255) / 256); }
+
+template <typename T, bool FULL>
+cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
+    const int planes = sizeof(T) == 4 ? 3 : 1;
+    CUtensorMap mp[2], mq[2];
+    PairArgs a{};
+    for (int i = 0; i < count; ++i) {
+        if (!operand_map(&mp[i], t[i].P, planes, t[i].Nn, t[i].K, t[i].p_mn, 128) ||
+            !operand_map(&mq[i], t[i].Q, planes, t[i].M, t[i].K, t[i].q_mn, 128))
+            return cudaErrorInvalidValue;
+        a.p[i] = prod_args(t[i]);
+        a.units[i] = pair_units(t[i]);
+    }
+    if (count == 1) {
+        mp[1] = mp[0];
+        mq[1] = mq[0];
+    }
+    constexpr int smem = kPairStages * 2 * 128 * kBK * 2 + 1024;
+    auto kern = linear_pair_kernel<T, FULL>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // pairs that fit the device at once, asked for once per device
+    static std::atomic<int> fit[64];
+    int dev = 0, pairs = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev < 64) pairs = fit[dev].load(std::memory_order_relaxed);
+    if (pairs == 0) {
+        pairs = num_sms / 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * pairs);
+        cfg.blockDim = dim3(kPairThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        int max_clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg) == cudaSuccess && max_clusters > 0 &&
+            max_clusters < pairs)
+            pairs = max_clusters;
+        (void)cudaGetLastError();
+        if (dev < 64) fit[dev].store(pairs, std::memory_order_relaxed);
+    }
+    const int total = a.units[0] + a.units[1];
+    if (pairs > total) pairs = total;
+    if (count == 2) {
+        // pairs [0, late) have one unit of the first product more than the others
+        a.late = a.units[0] % pairs;
+        a.early = a.late == 0 ? 0 : a.p[0].kb / a.p[1].kb;
+    }
+    a.timeout_ns = timeout_ns;
+    return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
+}
+
+template <typename T, int BN>
+cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStream_t s) {
+    const int planes = sizeof(T) == 4 ? 3 : 1;
+    CUtensorMap mp, mq;
+    if (!operand_map(&mp, t.P, planes, t.Nn, t.K, t.p_mn, 128) || !operand_map(&mq, t.Q, planes, t.M, t.K, t.q_mn, BN))
+        return cudaErrorInvalidValue;
+    const ProdArgs p = prod_args(t);
+    const int stage_bytes = 128 * kBK * 2 + split_b_bytes<BN>(t.q_mn);
+    int stages = (kSplitSmem - 1024) / stage_bytes;
+    if (stages > 6) stages = 6;
+    const int smem = 1024 + (stages * stage_bytes > BN * 512 ? stages * stage_bytes : BN * 512);
+    auto kern = linear_split_kernel<T, BN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + BN - 1) / BN);
+    if (tiles * S > INT32_MAX) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, mp, mq, p, S, stages, timeout_ns);
+}
+
+// Whether a product has tiles enough to run on CTA pairs.
+bool use_pairs(const TcProduct &t, int num_sms) { return pair_units(t) * 2 >= num_sms / 2; }
+
+template <typename T>
+cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
+    const int bn = t.M <= 16 ? 16 : t.M <= 32 ? 32 : t.M <= 64 ? 64 : 128;
+    const int64_t tiles = static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + bn - 1) / bn);
+    const int kb = (t.K + kBK - 1) / kBK;
+    int S = static_cast<int>(2 * num_sms / tiles);  // two CTAs an SM
+    if (S > 8) S = 8;
+    if (S > kb) S = kb;
+    if (S < 1) S = 1;
+    switch (bn) {
+    case 16: return launch_split<T, 16>(t, S, timeout_ns, s);
+    case 32: return launch_split<T, 32>(t, S, timeout_ns, s);
+    case 64: return launch_split<T, 64>(t, S, timeout_ns, s);
+    default: return launch_split<T, 128>(t, S, timeout_ns, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
+                               cudaStream_t s) {
+    bool pairs = true;
+    for (int i = 0; i < count; ++i) pairs = pairs && use_pairs(t[i], num_sms);
+    if (pairs) {
+        if (fp32)
+            return full ? launch_pair<float, true>(t, count, timeout_ns, num_sms, s)
+                        : launch_pair<float, false>(t, count, timeout_ns, num_sms, s);
+        return full ? launch_pair<__nv_bfloat16, true>(t, count, timeout_ns, num_sms, s)
+                    : launch_pair<__nv_bfloat16, false>(t, count, timeout_ns, num_sms, s);
+    }
+    for (int i = 0; i < count; ++i) {
+        cudaError_t e;
+        if (use_pairs(t[i], num_sms)) e = launch_tc_products(t + i, 1, fp32, full, timeout_ns, num_sms, s);
+        else e = fp32 ? run_split<float>(t[i], timeout_ns, num_sms, s) : run_split<__nv_bfloat16>(t[i], timeout_ns, num_sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace moe
