@@ -89,96 +89,163 @@ __device__ __forceinline__ void bf16_parts(float v, __nv_bfloat16 (&p)[3]) {
     p[2] = __float2bfloat16_rn(v);
 }
 
-// Writes element (r, c) of an operand: rows of ld elements, `plane` elements
-// from one part to the next (fp32).
+// Eight neighbouring elements of a row, in fp32: 16-byte loads when the rows are
+// whole vectors (vec), else one by one; zeros past the row's end.
 template <typename T>
-__device__ __forceinline__ void put_operand(__nv_bfloat16 *out, int64_t at, int64_t plane, float v) {
-    if constexpr (sizeof(T) == 4) {
-        __nv_bfloat16 p[3];
-        bf16_parts(v, p);
-        out[at] = p[0];
-        out[at + plane] = p[1];
-        out[at + 2 * plane] = p[2];
+__device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&v)[8]) {
+    if (vec) {
+        constexpr int W = sizeof(T) == 4 ? 2 : 1;
+        uint4 raw[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) raw[w] = *reinterpret_cast<const uint4 *>(row + c + w * (16 / static_cast<int>(sizeof(T))));
+        const T *e = reinterpret_cast<const T *>(raw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(e[i]);
     } else {
-        out[at] = __float2bfloat16_rn(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32<T>(row[c + i]) : 0.0f;
     }
 }
 
-// An array as an operand: rows padded with zeros to ld, fp32 values in parts.
+// Writes eight elements of an operand, a vector of each part; `plane` elements
+// from one part to the next (fp32).
 template <typename T>
+__device__ __forceinline__ void put_operand8(__nv_bfloat16 *out, int64_t at, int64_t plane, const float (&v)[8]) {
+    constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+    uint4 raw[PARTS];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (PARTS == 3) {
+            __nv_bfloat16 p[3];
+            bf16_parts(v[i], p);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) reinterpret_cast<__nv_bfloat16 *>(&raw[k])[i] = p[k];
+        } else {
+            reinterpret_cast<__nv_bfloat16 *>(&raw[0])[i] = __float2bfloat16_rn(v[i]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) *reinterpret_cast<uint4 *>(out + at + k * plane) = raw[k];
+}
+
+// An array as an operand: rows padded with zeros to ld (a multiple of 8), fp32
+// values in parts.  One thread per eight elements; I: index type that holds them all.
+template <typename T, typename I>
 __global__ void __launch_bounds__(256)
 linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __nv_bfloat16 *out) {
     pdl_trigger();
     pdl_wait();
-    const int64_t plane = rows * ld;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < plane; i += step) {
-        const int64_t r = i / ld;
-        const int c = static_cast<int>(i - r * ld);
-        put_operand<T>(out, i, plane, c < cols ? to_f32<T>(in[r * cols + c]) : 0.0f);
+    const bool vec = cols % 8 == 0;
+    const I per_row = static_cast<I>(ld / 8), total = static_cast<I>(rows) * per_row;
+    for (I i = static_cast<I>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<I>(gridDim.x) * 256) {
+        const I r = i / per_row;
+        const int c = static_cast<int>(i - r * per_row) * 8;
+        float v[8];
+        load8<T>(in + static_cast<int64_t>(r) * cols, c, cols, vec, v);
+        put_operand8<T>(out, static_cast<int64_t>(i) * 8, rows * ld, v);
     }
 }
 
 // ---------------------------------------------------------------- dZ and db
 // dZ = dy act'(z), rounded to the storage type and laid out as an operand, and
-// the column sums of the unrounded dZ over a chunk of rows.  A block takes 32
-// columns, its 8 warps every eighth row of the chunk.  dz and part nullable.
-// O: bf16 for an operand (fp32 in parts), T for the CUDA-core products.
+// the column sums of the unrounded dZ over a chunk of rows.  A block takes 256
+// columns, eight to a lane, its 8 warps every eighth row of the chunk, two at a
+// time.  dz and part nullable.  O: bf16 for an operand (fp32 in parts), T for
+// the CUDA-core products.
 template <typename T, typename O>
 __global__ void __launch_bounds__(256)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
                  int64_t chunk_rows, O *dz, float *part) {
-    __shared__ float red[8][33];
+    __shared__ float red[8][8][33];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    const int c = blockIdx.x * 256 + lane * 8;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * chunk_rows;
     const int64_t r1 = r0 + chunk_rows < M ? r0 + chunk_rows : M;
-    float a = 0.0f;
-    if (col < ld)
-        for (int64_t r = r0 + warp; r < r1; r += 8) {
-            float v = 0.0f;
-            if (col < n) {
-                v = to_f32<T>(dy[r * n + col]);
-                if (act != kActNone) v = act_backward(v, to_f32<T>(z[r * n + col]), act);
-                a += v;
+    const bool vec = n % 8 == 0;
+    float a[8] = {};
+    if (c < ld) {
+        for (int64_t r = r0 + warp; r < r1; r += 16) {
+            float v[2][8], u[2][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int64_t q = r + 8 * k;
+                if (q < r1) {
+                    load8<T>(dy + q * n, c, n, vec, v[k]);
+                    if (act != kActNone) load8<T>(z + q * n, c, n, vec, u[k]);
+                }
             }
-            if (dz != nullptr) {
-                if constexpr (sizeof(O) == sizeof(T)) dz[r * ld + col] = from_f32<T>(v);
-                else put_operand<T>(dz, r * ld + col, M * ld, v);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int64_t q = r + 8 * k;
+                if (q >= r1) break;
+                if (act == kActGelu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] = act_backward(v[k][i], u[k][i], kActGelu);
+                } else if (act == kActRelu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] = act_backward(v[k][i], u[k][i], kActRelu);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] += v[k][i];
+                if (dz != nullptr) {
+                    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c + i < n) dz[q * ld + c + i] = v[k][i];
+                    } else if (sizeof(T) == 2 && ld % 8 != 0) {  // bf16 rows for the CUDA cores
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c + i < n) dz[q * ld + c + i] = from_f32<O>(v[k][i]);
+                    } else {
+                        put_operand8<T>(reinterpret_cast<__nv_bfloat16 *>(dz), q * ld + c, M * ld, v[k]);
+                    }
+                }
             }
         }
+    }
     if (part == nullptr) return;
-    red[warp][lane] = a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[warp][i][lane] = a[i];
     __syncthreads();
-    if (warp == 0 && col < n) {
-        for (int w = 1; w < 8; ++w) a += red[w][lane];
-        part[static_cast<int64_t>(blockIdx.y) * n + col] = a;
+    const int col = blockIdx.x * 256 + threadIdx.x;  // this thread's column to finish
+    if (col < n) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += red[w][threadIdx.x & 7][threadIdx.x >> 3];
+        part[static_cast<int64_t>(blockIdx.y) * n + col] = s;
     }
 }
 
-__global__ void __launch_bounds__(256)
+// db = the chunks' sums added: 32 columns per block, each of 32 warps every 32nd
+// chunk, then a tree over the warps.
+__global__ void __launch_bounds__(1024)
 linear_db_kernel(const float *part, int64_t groups, int n, float *db) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float a = 0.0f;
-    if (col < n)
-        for (int64_t g = warp; g < groups; g += 8) a += part[g * n + col];
+    if (col < n) {
+#pragma unroll 4
+        for (int64_t g = warp; g < groups; g += 32) a += part[g * n + col];
+    }
     red[warp][lane] = a;
     __syncthreads();
-    if (warp == 0 && col < n) {
-        for (int w = 1; w < 8; ++w) a += red[w][lane];
-        db[col] = a;
-    }
+    a = red[lane][warp];  // warp w now sums column w
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < n) db[blockIdx.x * 32 + warp] = a;
 }
 
-int64_t row_chunks(int64_t M) {
-    int64_t c = (M + 255) / 256;
-    return c < 1 ? 1 : c > 64 ? 64 : c;
+// Chunks of rows of the dZ pass: about four blocks an SM, at least 32 rows each.
+int64_t row_chunks(int64_t M, int n) {
+    const int64_t tiles = (static_cast<int64_t>(n) + 255) / 256;
+    int64_t c = 592 / tiles;
+    if (c > (M + 31) / 32) c = (M + 31) / 32;
+    return c < 1 ? 1 : c;
 }
 
 }  // namespace
@@ -198,10 +265,11 @@ size_t operand_bytes(int64_t rows, int cols, int dt) {
 template <typename T>
 cudaError_t pack(const void *&in, int64_t rows, int cols, void *out, cudaStream_t s) {
     if (!needs_pack(sizeof(T) == 2 ? 1 : 0, cols)) return cudaSuccess;
-    const int64_t n = rows * pad8(cols), blocks = (n + 1023) / 1024;
-    cudaError_t e = launch_pdl(linear_pack_kernel<T>, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)),
-                               dim3(256), 0, s, static_cast<const T *>(in), rows, cols, pad8(cols),
-                               static_cast<__nv_bfloat16 *>(out));
+    const int64_t n = rows * (pad8(cols) / 8), blocks = (n + 255) / 256;
+    const bool small = n + 256 * 2368 < UINT32_MAX;
+    cudaError_t e = launch_pdl(small ? linear_pack_kernel<T, uint32_t> : linear_pack_kernel<T, int64_t>,
+                               dim3(static_cast<unsigned>(blocks < 2368 ? blocks : 2368)), dim3(256), 0, s,
+                               static_cast<const T *>(in), rows, cols, pad8(cols), static_cast<__nv_bfloat16 *>(out));
     in = out;
     return e;
 }
@@ -240,7 +308,7 @@ BwdScratch bwd_scratch(int64_t M, int d_in, int d_out, int dt, int act) {
     L.W = o;
     if (!simt && needs_pack(dt, d_in)) o += operand_bytes(d_out, d_in, dt);
     L.part = o;
-    o += align_up(static_cast<size_t>(row_chunks(M)) * d_out * sizeof(float), 256);
+    o += align_up(static_cast<size_t>(row_chunks(M, d_out)) * d_out * sizeof(float), 256);
     L.total = o;
     return L;
 }
@@ -291,12 +359,12 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         const bool products = a.dx != nullptr || a.dW != nullptr;
         const bool make_dz = products && (a.act != kActNone || (!simt && needs_pack(a.dt, a.d_out)));
         float *part = a.db != nullptr ? reinterpret_cast<float *>(w + L.part) : nullptr;
-        const int64_t chunks = row_chunks(a.M);
+        const int64_t chunks = row_chunks(a.M, a.d_out);
         const void *dz = make_dz ? static_cast<const void *>(w + L.dz) : a.dy;
         if (make_dz || part != nullptr) {
             // on CUDA cores dZ stays in the storage type; otherwise it is laid out as an operand
             const int ld = simt ? a.d_out : pad8(a.d_out);
-            const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(ld) + 31) / 32), static_cast<unsigned>(chunks));
+            const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(ld) + 255) / 256), static_cast<unsigned>(chunks));
             if (simt)
                 e = launch_pdl(linear_dz_kernel<T, T>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
                                static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
@@ -309,7 +377,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         }
         if (part != nullptr) {
             e = launch_pdl(linear_db_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(a.d_out) + 31) / 32)),
-                           dim3(256), 0, s, part, chunks, a.d_out, a.db);
+                           dim3(1024), 0, s, part, chunks, a.d_out, a.db);
             if (e != cudaSuccess) return e;
         }
         if (!products) return e;

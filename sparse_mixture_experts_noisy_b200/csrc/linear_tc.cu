@@ -16,10 +16,11 @@
 // bf16 parts, v = v0 + v1 + v2 (8 significant bits each), stored as three
 // planes, and the six products of parts p, q with p + q <= 2 are summed; the
 // three that are left out are below 2^-24 of the product.  Each product of two
-// parts is exact in fp32.  The tensor core truncates when it adds to its
-// accumulator, an error that grows with the number of additions, so K is cut
-// into pieces of kPieceKb blocks: each starts from zero, takes the five small
-// products before the large one, and is added to the others in registers.
+// parts is exact in fp32.  A K block's three planes of both operands are loaded
+// together and serve all six products.  The tensor core truncates when it adds
+// to its accumulator, an error that grows with the number of additions, so K is
+// cut into pieces of kPieceKb blocks: each starts from zero and is added to the
+// others in registers.
 #include <atomic>
 
 #include "common.cuh"
@@ -45,8 +46,8 @@ cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
 namespace {
 
 constexpr int kBK = 64;        // K elements per stage: 128 bytes, one swizzle row
-constexpr int kPieceKb = 16;   // K blocks per piece of an fp32 product
-constexpr int kTerms = 6;      // products of parts, the largest last
+constexpr int kPieceKb = 4;    // K blocks per piece of an fp32 product
+constexpr int kTerms = 6;      // products of parts
 
 // Plane of P and of Q for term t: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
 __device__ __forceinline__ int term_p(int t) { return t == 1 ? 2 : (t == 2 || t == 4) ? 1 : 0; }
@@ -78,44 +79,60 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 
 // Stores up to CN accumulated columns (rows m0.. of D, `cols` of them valid) of
 // this lane's n.  FULL: bias, activation, residual and z as the epilogue says;
-// otherwise the value alone.
-template <typename T, bool FULL, int CN>
-__device__ __forceinline__ void store_cols(const LinearEpi &e, const float *v, int64_t m0, int n, int ld, int cols,
-                                           float bias) {
-    int64_t at = m0 * ld + n;
-    T *out = static_cast<T *>(e.out);
-    if constexpr (!FULL) {
+// otherwise the value alone.  Every choice is made once for the CN columns: a
+// branch per element made a 256 x 256 tile's epilogue take 20 us.
+template <typename T, int CN>
+__device__ __forceinline__ void put_cols(T *p, const float (&v)[CN], int ld, int cols) {
+    if (cols >= CN) {
 #pragma unroll
-        for (int i = 0; i < CN; ++i, at += ld)
-            if (i < cols) out[at] = from_f32<T>(v[i]);
+        for (int i = 0; i < CN; ++i) p[static_cast<int64_t>(i) * ld] = from_f32<T>(v[i]);
     } else {
-        float res[CN];
+#pragma unroll
+        for (int i = 0; i < CN; ++i)
+            if (i < cols) p[static_cast<int64_t>(i) * ld] = from_f32<T>(v[i]);
+    }
+}
+
+template <typename T, bool FULL, int CN>
+__device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc, int64_t m0, int n, int ld, int cols,
+                                           float bias) {
+    const int64_t at = m0 * ld + n;
+    T *out = static_cast<T *>(e.out) + at;
+    float v[CN];
+#pragma unroll
+    for (int i = 0; i < CN; ++i) v[i] = acc[i];
+    if constexpr (FULL) {
+        T res[CN];
         if (e.residual != nullptr) {
             const T *p = static_cast<const T *>(e.residual) + at;
 #pragma unroll
-            for (int i = 0; i < CN; ++i) {
-                res[i] = i < cols ? to_f32<T>(*p) : 0.0f;
-                p += ld;
-            }
+            for (int i = 0; i < CN; ++i) res[i] = p[static_cast<int64_t>(i < cols ? i : 0) * ld];
         }
 #pragma unroll
-        for (int i = 0; i < CN; ++i, at += ld) {
-            if (i < cols) {
-                float u = v[i] + bias;
-                if (e.z_out != nullptr) static_cast<T *>(e.z_out)[at] = from_f32<T>(u);
-                u = act_value(u, e.act);
-                if (e.residual != nullptr) u += res[i];
-                out[at] = from_f32<T>(u);
-            }
+        for (int i = 0; i < CN; ++i) v[i] += bias;
+        if (e.z_out != nullptr) put_cols<T, CN>(static_cast<T *>(e.z_out) + at, v, ld, cols);
+        if (e.act == kActGelu) {
+#pragma unroll
+            for (int i = 0; i < CN; ++i) v[i] = act_value(v[i], kActGelu);
+        } else if (e.act == kActRelu) {
+#pragma unroll
+            for (int i = 0; i < CN; ++i) v[i] = act_value(v[i], kActRelu);
+        }
+        if (e.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < CN; ++i) v[i] += to_f32<T>(res[i]);
         }
     }
+    put_cols<T, CN>(out, v, ld, cols);
 }
 
 // ---------------------------------------------------------------- CTA pairs
 // A pair of CTAs (tcgen05 cta_group::2) computes 256 x 256 tiles of D: CTA r
 // loads P rows [n0 + 128 r, +128) and Q rows [m0 + 128 r, +128) per K block, the
 // leader's MMA reads both, and each CTA's tensor memory gets its 128 n of all
-// 256 m.  Persistent, one pair per two SMs; two accumulators, so the epilogue of
+// 256 m.  fp32 tiles are 256 n x 128 m: an epilogue thread then adds 64 columns in
+// registers, and six products per load keep L2 traffic low all the same.
+// Persistent, one pair per two SMs; two accumulators, so the epilogue of
 // one tile (or piece) overlaps the MMAs of the next.  Warp 0: TMA; warp 1: MMA;
 // warps 2-9: epilogue, two groups of four, each half of the m.
 //
@@ -124,7 +141,9 @@ __device__ __forceinline__ void store_cols(const LinearEpi &e, const float *v, i
 // with the pairs that got one fewer of the first's, as many as fit into the time
 // the others still need, before they are dealt to all.
 constexpr int kPairThreads = 320;
-constexpr int kPairStages = 6;
+constexpr int pair_tile_m(bool fp32) { return fp32 ? 128 : 256; }
+constexpr int pair_stages(bool fp32) { return fp32 ? 3 : 6; }
+constexpr int pair_stage_bytes(bool fp32) { return fp32 ? 3 * (128 + 64) * kBK * 2 : (128 + 128) * kBK * 2; }
 constexpr int kGroupM = 8;  // m tiles that share a sweep over n: their Q rows stay in L2
 
 struct PairArgs {
@@ -139,6 +158,7 @@ struct PairUnit {
     int64_t m0;
 };
 
+template <int TM>
 __device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npairs, int i, PairUnit &t) {
     const int n1 = pair < a.units[0] ? (a.units[0] - pair + npairs - 1) / npairs : 0;
     int u;
@@ -157,11 +177,11 @@ __device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npair
         if (u >= a.units[1]) return false;
     }
     const ProdArgs &p = a.p[t.prob];
-    const int mt = static_cast<int>((p.M + 255) / 256), nt = (p.Nn + 255) / 256;
+    const int mt = static_cast<int>((p.M + TM - 1) / TM), nt = (p.Nn + 255) / 256;
     const int sweep = kGroupM * nt;
     const int grp = u / sweep, rem = u - grp * sweep;
     const int rows = mt - grp * kGroupM < kGroupM ? mt - grp * kGroupM : kGroupM;
-    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * 256;
+    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * TM;
     t.n0 = rem / rows * 256;
     return true;
 }
@@ -172,9 +192,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                    const __grid_constant__ CUtensorMap tp1, const __grid_constant__ CUtensorMap tq1,
                    const __grid_constant__ PairArgs args) {
     constexpr bool SPLIT = sizeof(T) == 4;
-    constexpr int TERMS = SPLIT ? kTerms : 1;
-    constexpr int STAGES = kPairStages;
-    constexpr uint32_t A_BYTES = 128 * kBK * 2, STAGE_BYTES = 2 * A_BYTES;
+    constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
+    constexpr int TM = pair_tile_m(SPLIT), QR = TM / 2, HALF = TM / 2;  // Q rows a CTA; m an epilogue group
+    constexpr int STAGES = pair_stages(SPLIT);
+    constexpr uint32_t P_BYTES = 128 * kBK * 2, Q_BYTES = QR * kBK * 2, Q_AT = PLANES * P_BYTES;
+    constexpr uint32_t STAGE_BYTES = pair_stage_bytes(SPLIT);
+    static_assert(STAGE_BYTES == PLANES * (P_BYTES + Q_BYTES) && STAGE_BYTES % 1024 == 0, "stage");
 
     extern __shared__ uint8_t dyn_smem[];
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
@@ -227,43 +250,40 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             bool ok = true;
             const uint64_t pol = policy_evict_normal();
             PairUnit t;
-            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+            for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
                 const ProdArgs &p = args.p[t.prob];
                 const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
                 const int nr = t.n0 + static_cast<int>(rank) * 128;
-                const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * 128;
-                const int piece = SPLIT ? kPieceKb : p.kb;
-                for (int k0 = 0; k0 < p.kb && ok; k0 += piece) {
-                    const int k1 = k0 + piece < p.kb ? k0 + piece : p.kb;
-                    for (int x = 0; x < TERMS && ok; ++x) {
-                        const int zp = SPLIT ? term_p(x) : 0, zq = SPLIT ? term_q(x) : 0;
-                        for (int kb = k0; kb < k1; ++kb) {
-                            if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 61)) {
-                                ok = false;
-                                break;
-                            }
-                            if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
-                            const uint32_t fb = full0_lead + 8 * stage;
-                            const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                            const int kx = kb * kBK;
-                            if (p.p_mn) {
-                                tma_load_3d_pair(sa, tp, fb, nr, kx, zp, pol);
-                                tma_load_3d_pair(sa + 8192u, tp, fb, nr + 64, kx, zp, pol);
-                            } else {
-                                tma_load_3d_pair(sa, tp, fb, kx, nr, zp, pol);
-                            }
-                            if (p.q_mn) {
-                                tma_load_3d_pair(sa + A_BYTES, tq, fb, mr, kx, zq, pol);
-                                tma_load_3d_pair(sa + A_BYTES + 8192u, tq, fb, mr + 64, kx, zq, pol);
-                            } else {
-                                tma_load_3d_pair(sa + A_BYTES, tq, fb, kx, mr, zq, pol);
-                            }
-                            ++issued;
-                            if (++stage == STAGES) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
+                const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * QR;
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 61)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+                    const uint32_t fb = full0_lead + 8 * stage;
+                    const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                    const int kx = kb * kBK;
+#pragma unroll
+                    for (int z = 0; z < PLANES; ++z) {
+                        const uint32_t a = sa + z * P_BYTES, b = sa + Q_AT + z * Q_BYTES;
+                        if (p.p_mn) {
+                            tma_load_3d_pair(a, tp, fb, nr, kx, z, pol);
+                            tma_load_3d_pair(a + 8192u, tp, fb, nr + 64, kx, z, pol);
+                        } else {
+                            tma_load_3d_pair(a, tp, fb, kx, nr, z, pol);
                         }
+                        if (p.q_mn) {
+                            tma_load_3d_pair(b, tq, fb, mr, kx, z, pol);
+                            if constexpr (QR == 128) tma_load_3d_pair(b + 8192u, tq, fb, mr + 64, kx, z, pol);
+                        } else {
+                            tma_load_3d_pair(b, tq, fb, kx, mr, z, pol);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -288,23 +308,23 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             uint32_t phase = 0;
             bool ok = true, any = false;
             PairUnit t;
-            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+            for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
                 const ProdArgs &p = args.p[t.prob];
                 const bool pm = p.p_mn != 0, qm = p.q_mn != 0;
-                const uint32_t idesc = idesc_bf16_f32(256, 256) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
+                const uint32_t idesc = idesc_bf16_f32(256, TM) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
                 // K-major: the next 16 of K are 32 bytes on in the swizzled row;
                 // MN-major: 16 rows of 128 bytes on
                 const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
                 const int piece = SPLIT ? kPieceKb : p.kb;
                 for (int k0 = 0; k0 < p.kb && ok; k0 += piece) {
-                    const int n = (k0 + piece < p.kb ? piece : p.kb - k0) * TERMS;
+                    const int n = k0 + piece < p.kb ? piece : p.kb - k0;
                     const int acc = local & 1;
                     if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 62)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TM);
                     for (int k = 0; k < n; ++k) {
                         if (!mbar_wait_bounded(full0 + 8 * stage, phase, status, tmo, 63)) {
                             ok = false;
@@ -313,11 +333,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                         tc_fence_after();
                         const uint32_t sa = smem_base + stage * STAGE_BYTES;
                         const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
-                        const uint64_t bd = qm ? smem_desc_mn_sw128(sa + A_BYTES, 8192u, 1024u)
-                                               : smem_desc_sw128(sa + A_BYTES);
+                        const uint64_t bd = qm ? smem_desc_mn_sw128(sa + Q_AT, 8192u, 1024u) : smem_desc_sw128(sa + Q_AT);
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            umma_bf16_pair(d_tmem, ad + astep * kk, bd + bstep * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                        for (int x = 0; x < TERMS; ++x) {
+                            const uint64_t ax = ad + (SPLIT ? term_p(x) * (P_BYTES >> 4) : 0);
+                            const uint64_t bx = bd + (SPLIT ? term_q(x) * (Q_BYTES >> 4) : 0);
+#pragma unroll
+                            for (int kk = 0; kk < kBK / 16; ++kk)
+                                umma_bf16_pair(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                               (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                        }
                         any = true;
                         umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
                         if (++stage == STAGES) {
@@ -340,14 +365,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         int local = 0;
         bool ok = true;
         PairUnit t;
-        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+        for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
             const ProdArgs &p = args.p[t.prob];
             const int n = t.n0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-            const int64_t m0 = t.m0 + half * 128;
+            const int64_t m0 = t.m0 + half * HALF;
             const int64_t left = p.M - m0;
-            const int rows = left < 128 ? static_cast<int>(left > 0 ? left : 0) : 128;
+            const int rows = left < HALF ? static_cast<int>(left > 0 ? left : 0) : HALF;
             const float bias = (FULL && p.epi.bias != nullptr && n < p.Nn) ? p.epi.bias[n] : 0.0f;
-            float sum[SPLIT ? 128 : 1];
+            float sum[SPLIT ? HALF : 1];
             const int pieces = SPLIT ? (p.kb + kPieceKb - 1) / kPieceKb : 1;
             for (int pc = 0; pc < pieces; ++pc) {
                 const int acc = local & 1;
@@ -357,10 +382,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                 }
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                       static_cast<uint32_t>(acc * 256 + half * 128);
+                                       static_cast<uint32_t>(acc * TM + half * HALF);
                 if constexpr (SPLIT) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < HALF / 16; ++c) {
                         uint32_t r[16];
                         tmem_ld_32x32b_x16(taddr + c * 16, r);
                         tmem_wait_ld();
@@ -389,9 +414,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             if constexpr (SPLIT) {
                 if (ok && n < p.Nn) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (c * 8 < rows)
-                            store_cols<T, FULL, 8>(p.epi, sum + c * 8, m0 + c * 8, n, p.Nn, rows - c * 8, bias);
+                    for (int c = 0; c < HALF / 16; ++c)
+                        if (c * 16 < rows)
+                            store_cols<T, FULL, 16>(p.epi, sum + c * 16, m0 + c * 16, n, p.Nn, rows - c * 16, bias);
                 }
             }
         }
@@ -412,24 +437,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
 // memory, and after a cluster barrier CTA r adds the S parts of its share of the
 // columns in order (through distributed shared memory) and stores them.  Small
 // batches stream W this way: BN is the batch rounded up to 16, 32, 64 or 128.
-// Two CTAs fit an SM, so one's start and end overlap the other's copies.
+// Two bf16 CTAs fit an SM, so one's start and end overlap the other's copies; an
+// fp32 stage (three planes) needs the whole SM.
 constexpr int kSplitThreads = 192;
-constexpr int kSplitSmem = 108 * 1024;
+constexpr int split_ctas(bool fp32) { return fp32 ? 1 : 2; }
+constexpr int kSplitSmem = 216 * 1024;
 
 template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
 
 template <typename T, int BN>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+__global__ void __launch_bounds__(kSplitThreads, split_ctas(sizeof(T) == 4))
 linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constant__ CUtensorMap tq, const ProdArgs p,
                     const int S, const int stages, const uint64_t tmo) {
     constexpr bool SPLIT = sizeof(T) == 4;
-    constexpr int TERMS = SPLIT ? kTerms : 1;
+    constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
     constexpr int COLS = BN < 32 ? 32 : BN;  // tensor-memory columns of one accumulator
     constexpr uint32_t TMEM_COLS = 2 * COLS;
     constexpr uint32_t A_BYTES = 128 * kBK * 2;
     constexpr int kMaxStages = 6;
     const uint32_t b_bytes = split_b_bytes<BN>(p.q_mn != 0);
-    const uint32_t stage_bytes = A_BYTES + b_bytes;
+    const uint32_t stage_bytes = PLANES * (A_BYTES + b_bytes);
 
     extern __shared__ uint8_t dyn_smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
@@ -485,36 +512,34 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int k0 = kb0; k0 < kb1 && ok; k0 += piece) {
-                const int k1 = k0 + piece < kb1 ? k0 + piece : kb1;
-                for (int x = 0; x < TERMS && ok; ++x) {
-                    const int zp = SPLIT ? term_p(x) : 0, zq = SPLIT ? term_q(x) : 0;
-                    for (int kb = k0; kb < k1; ++kb) {
-                        if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 71)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
-                        mbar_arrive_expect_tx(fb, stage_bytes);
-                        const int kx = kb * kBK, mr = static_cast<int>(m0);
-                        if (p.p_mn) {
-                            tma_load_3d(sa, &tp, fb, n0, kx, zp);
-                            tma_load_3d(sa + 8192u, &tp, fb, n0 + 64, kx, zp);
-                        } else {
-                            tma_load_3d(sa, &tp, fb, kx, n0, zp);
-                        }
-                        if (p.q_mn) {
-                            tma_load_3d(sa + A_BYTES, &tq, fb, mr, kx, zq);
-                            if constexpr (BN == 128) tma_load_3d(sa + A_BYTES + 8192u, &tq, fb, mr + 64, kx, zq);
-                        } else {
-                            tma_load_3d(sa + A_BYTES, &tq, fb, kx, mr, zq);
-                        }
-                        ++issued;
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 71)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
+                mbar_arrive_expect_tx(fb, stage_bytes);
+                const int kx = kb * kBK, mr = static_cast<int>(m0);
+#pragma unroll
+                for (int z = 0; z < PLANES; ++z) {
+                    const uint32_t a = sa + z * A_BYTES, b = sa + PLANES * A_BYTES + z * b_bytes;
+                    if (p.p_mn) {
+                        tma_load_3d(a, &tp, fb, n0, kx, z);
+                        tma_load_3d(a + 8192u, &tp, fb, n0 + 64, kx, z);
+                    } else {
+                        tma_load_3d(a, &tp, fb, kx, n0, z);
                     }
+                    if (p.q_mn) {
+                        tma_load_3d(b, &tq, fb, mr, kx, z);
+                        if constexpr (BN == 128) tma_load_3d(b + 8192u, &tq, fb, mr + 64, kx, z);
+                    } else {
+                        tma_load_3d(b, &tq, fb, kx, mr, z);
+                    }
+                }
+                ++issued;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
             if (!ok) {
@@ -540,7 +565,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
             const uint32_t idesc = idesc_bf16_f32(128, BN) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
             const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
             for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++local) {
-                const int n = (k0 + piece < kb1 ? piece : kb1 - k0) * TERMS;
+                const int n = k0 + piece < kb1 ? piece : kb1 - k0;
                 const int acc = local & 1;
                 if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 72)) {
                     ok = false;
@@ -555,11 +580,18 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_base + stage * stage_bytes;
+                    const uint32_t sb = sa + PLANES * A_BYTES;
                     const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
-                    const uint64_t bd = qm ? smem_desc_mn_sw128(sa + A_BYTES, 8192u, 1024u) : smem_desc_sw128(sa + A_BYTES);
+                    const uint64_t bd = qm ? smem_desc_mn_sw128(sb, 8192u, 1024u) : smem_desc_sw128(sb);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16(d_tmem, ad + astep * kk, bd + bstep * kk, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                    for (int x = 0; x < TERMS; ++x) {
+                        const uint64_t ax = ad + (SPLIT ? term_p(x) * (A_BYTES >> 4) : 0);
+                        const uint64_t bx = bd + (SPLIT ? term_q(x) * (b_bytes >> 4) : 0);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            umma_bf16(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                      (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                    }
                     any = true;
                     umma_commit(empty0 + 8 * stage);
                     if (++stage == stages) {
@@ -660,7 +692,10 @@ bool operand_map(CUtensorMap *m, const void *base, int planes, int64_t rows, int
     return make_tmap_bf16_3d(m, base, planes, static_cast<int>(outer), static_cast<int>(inner), mn ? 64 : box);
 }
 
-int pair_units(const TcProduct &t) { return static_cast<int>((t.M + 255) / 256) * ((t.Nn + 255) / 256); }
+int pair_units(const TcProduct &t, bool fp32) {
+    const int tm = pair_tile_m(fp32);
+    return static_cast<int>((t.M + tm - 1) / tm) * ((t.Nn + 255) / 256);
+}
 
 template <typename T, bool FULL>
 cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
@@ -669,16 +704,16 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     PairArgs a{};
     for (int i = 0; i < count; ++i) {
         if (!operand_map(&mp[i], t[i].P, planes, t[i].Nn, t[i].K, t[i].p_mn, 128) ||
-            !operand_map(&mq[i], t[i].Q, planes, t[i].M, t[i].K, t[i].q_mn, 128))
+            !operand_map(&mq[i], t[i].Q, planes, t[i].M, t[i].K, t[i].q_mn, pair_tile_m(sizeof(T) == 4) / 2))
             return cudaErrorInvalidValue;
         a.p[i] = prod_args(t[i]);
-        a.units[i] = pair_units(t[i]);
+        a.units[i] = pair_units(t[i], sizeof(T) == 4);
     }
     if (count == 1) {
         mp[1] = mp[0];
         mq[1] = mq[0];
     }
-    constexpr int smem = kPairStages * 2 * 128 * kBK * 2 + 1024;
+    constexpr int smem = pair_stages(sizeof(T) == 4) * pair_stage_bytes(sizeof(T) == 4) + 1024;
     auto kern = linear_pair_kernel<T, FULL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -706,7 +741,7 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     if (count == 2) {
         // pairs [0, late) have one unit of the first product more than the others
         a.late = a.units[0] % pairs;
-        a.early = a.late == 0 ? 0 : a.p[0].kb / a.p[1].kb;
+        a.early = a.late == 0 ? 0 : (a.p[0].kb + a.p[1].kb / 2) / a.p[1].kb;
     }
     a.timeout_ns = timeout_ns;
     return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
@@ -719,8 +754,8 @@ cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStr
     if (!operand_map(&mp, t.P, planes, t.Nn, t.K, t.p_mn, 128) || !operand_map(&mq, t.Q, planes, t.M, t.K, t.q_mn, BN))
         return cudaErrorInvalidValue;
     const ProdArgs p = prod_args(t);
-    const int stage_bytes = 128 * kBK * 2 + split_b_bytes<BN>(t.q_mn);
-    int stages = (kSplitSmem - 1024) / stage_bytes;
+    const int stage_bytes = planes * (128 * kBK * 2 + split_b_bytes<BN>(t.q_mn));
+    int stages = (kSplitSmem / split_ctas(sizeof(T) == 4) - 1024) / stage_bytes;
     if (stages > 6) stages = 6;
     const int smem = 1024 + (stages * stage_bytes > BN * 512 ? stages * stage_bytes : BN * 512);
     auto kern = linear_split_kernel<T, BN>;
@@ -746,14 +781,14 @@ cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStr
 }
 
 // Whether a product has tiles enough to run on CTA pairs.
-bool use_pairs(const TcProduct &t, int num_sms) { return pair_units(t) * 2 >= num_sms / 2; }
+bool use_pairs(const TcProduct &t, bool fp32, int num_sms) { return pair_units(t, fp32) * 2 >= num_sms / 2; }
 
 template <typename T>
 cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
     const int bn = t.M <= 16 ? 16 : t.M <= 32 ? 32 : t.M <= 64 ? 64 : 128;
     const int64_t tiles = static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + bn - 1) / bn);
     const int kb = (t.K + kBK - 1) / kBK;
-    int S = static_cast<int>(2 * num_sms / tiles);  // two CTAs an SM
+    int S = static_cast<int>(split_ctas(sizeof(T) == 4) * num_sms / tiles);
     if (S > 8) S = 8;
     if (S > kb) S = kb;
     if (S < 1) S = 1;
@@ -770,7 +805,7 @@ cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cuda
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s) {
     bool pairs = true;
-    for (int i = 0; i < count; ++i) pairs = pairs && use_pairs(t[i], num_sms);
+    for (int i = 0; i < count; ++i) pairs = pairs && use_pairs(t[i], fp32, num_sms);
     if (pairs) {
         if (fp32)
             return full ? launch_pair<float, true>(t, count, timeout_ns, num_sms, s)
@@ -780,7 +815,7 @@ cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool fu
     }
     for (int i = 0; i < count; ++i) {
         cudaError_t e;
-        if (use_pairs(t[i], num_sms)) e = launch_tc_products(t + i, 1, fp32, full, timeout_ns, num_sms, s);
+        if (use_pairs(t[i], fp32, num_sms)) e = launch_tc_products(t + i, 1, fp32, full, timeout_ns, num_sms, s);
         else e = fp32 ? run_split<float>(t[i], timeout_ns, num_sms, s) : run_split<__nv_bfloat16>(t[i], timeout_ns, num_sms, s);
         if (e != cudaSuccess) return e;
     }
