@@ -89,23 +89,24 @@ __device__ __forceinline__ void bf16_parts(float v, __nv_bfloat16 (&p)[3]) {
     p[2] = __float2bfloat16_rn(v);
 }
 
-// Eight neighbouring elements of a row, in fp32: 16-byte loads when the rows are
-// whole vectors (vec), else one by one; zeros past the row's end.
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&v)[8]) {
-    if (vec) {
-        constexpr int W = sizeof(T) == 4 ? 2 : 1;
-        uint4 raw[W];
+// Eight neighbouring elements of a row: 16-byte loads when the rows are whole
+// vectors (vec), else one by one; zeros past the row's end.
+template <typename T> struct Eight {
+    static constexpr int W = sizeof(T) == 4 ? 2 : 1;
+    uint4 raw[W];
+    __device__ __forceinline__ void load(const T *row, int c, int cols, bool vec) {
+        if (vec) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) raw[w] = *reinterpret_cast<const uint4 *>(row + c + w * (16 / static_cast<int>(sizeof(T))));
-        const T *e = reinterpret_cast<const T *>(raw);
+            for (int w = 0; w < W; ++w)
+                raw[w] = *reinterpret_cast<const uint4 *>(row + c + w * (16 / static_cast<int>(sizeof(T))));
+        } else {
+            T *e = reinterpret_cast<T *>(raw);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32<T>(row[c + i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? row[c + i] : from_f32<T>(0.0f);
+        }
     }
-}
+    __device__ __forceinline__ float operator[](int i) const { return to_f32<T>(reinterpret_cast<const T *>(raw)[i]); }
+};
 
 // Writes eight elements of an operand, a vector of each part; `plane` elements
 // from one part to the next (fp32).
@@ -140,8 +141,11 @@ linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __n
     for (I i = static_cast<I>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<I>(gridDim.x) * 256) {
         const I r = i / per_row;
         const int c = static_cast<int>(i - r * per_row) * 8;
+        Eight<T> in8;
+        in8.load(in + static_cast<int64_t>(r) * cols, c, cols, vec);
         float v[8];
-        load8<T>(in + static_cast<int64_t>(r) * cols, c, cols, vec, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = in8[k];
         put_operand8<T>(out, static_cast<int64_t>(i) * 8, rows * ld, v);
     }
 }
@@ -149,13 +153,14 @@ linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __n
 // ---------------------------------------------------------------- dZ and db
 // dZ = dy act'(z), rounded to the storage type and laid out as an operand, and
 // the column sums of the unrounded dZ over a chunk of rows.  A block takes 256
-// columns, eight to a lane, its 8 warps every eighth row of the chunk, two at a
+// columns, eight to a lane, its 8 warps every eighth row of the chunk, ROWS at a
 // time.  dz and part nullable.  O: bf16 for an operand (fp32 in parts), T for
 // the CUDA-core products.
 template <typename T, typename O>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
                  int64_t chunk_rows, O *dz, float *part) {
+    constexpr int ROWS = sizeof(T) == 4 ? 2 : 4;  // rows a lane has in flight
     __shared__ float red[8][8][33];
     pdl_trigger();
     pdl_wait();
@@ -166,40 +171,39 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int
     const bool vec = n % 8 == 0;
     float a[8] = {};
     if (c < ld) {
-        for (int64_t r = r0 + warp; r < r1; r += 16) {
-            float v[2][8], u[2][8];
+        for (int64_t r = r0 + warp; r < r1; r += 8 * ROWS) {
+            Eight<T> v8[ROWS], z8[ROWS];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < ROWS; ++k) {
                 const int64_t q = r + 8 * k;
                 if (q < r1) {
-                    load8<T>(dy + q * n, c, n, vec, v[k]);
-                    if (act != kActNone) load8<T>(z + q * n, c, n, vec, u[k]);
+                    v8[k].load(dy + q * n, c, n, vec);
+                    if (act != kActNone) z8[k].load(z + q * n, c, n, vec);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < ROWS; ++k) {
                 const int64_t q = r + 8 * k;
                 if (q >= r1) break;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = v8[k][i];
                 if (act == kActGelu) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[k][i] = act_backward(v[k][i], u[k][i], kActGelu);
+                    for (int i = 0; i < 8; ++i) v[i] = act_backward(v[i], z8[k][i], kActGelu);
                 } else if (act == kActRelu) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[k][i] = act_backward(v[k][i], u[k][i], kActRelu);
+                    for (int i = 0; i < 8; ++i) v[i] = act_backward(v[i], z8[k][i], kActRelu);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] += v[k][i];
+                for (int i = 0; i < 8; ++i) a[i] += v[i];
                 if (dz != nullptr) {
-                    if constexpr (sizeof(O) == 4) {
+                    if (sizeof(O) == 4 || (sizeof(T) == 2 && ld % 8 != 0)) {  // plain rows for the CUDA cores
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (c + i < n) dz[q * ld + c + i] = v[k][i];
-                    } else if (sizeof(T) == 2 && ld % 8 != 0) {  // bf16 rows for the CUDA cores
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c + i < n) dz[q * ld + c + i] = from_f32<O>(v[k][i]);
+                            if (c + i < n) dz[q * ld + c + i] = from_f32<O>(v[i]);
                     } else {
-                        put_operand8<T>(reinterpret_cast<__nv_bfloat16 *>(dz), q * ld + c, M * ld, v[k]);
+                        put_operand8<T>(reinterpret_cast<__nv_bfloat16 *>(dz), q * ld + c, M * ld, v);
                     }
                 }
             }

@@ -7,9 +7,30 @@ namespace moe {
 
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2 };
 
+// Phi(z) of the standard normal, and e = exp(-z^2 / 2), from one exponential:
+// 1 - erf(x) = (a1 t + ... + a5 t^5) exp(-x^2) with t = 1 / (1 + 0.3275911 x),
+// x = |z| / sqrt(2) >= 0 (Abramowitz and Stegun, 7.1.26; error of erf below
+// 1.5e-7, about that of fp32's 1 + erf).  Calling erff and expf instead made the
+// GELU passes bound by arithmetic: 113 us against 28 us of bytes for db at
+// 32768 x 1408.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float x = fabsf(z) * 0.70710678118654752440f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = __expf(-x * x);
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float tail = 0.5f * p * t * e;  // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 // ReLU keeps a NaN (v < 0 is false for it).
 __device__ __forceinline__ float act_value(float v, int act) {
-    if (act == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752440f));
+    if (act == kActGelu) {
+        float e;
+        return __fmul_rn(v, normal_cdf(v, e));  // by itself: the same bits with and without a residual or z
+    }
     if (act == kActRelu) return v < 0.0f ? 0.0f : v;
     return v;
 }
@@ -18,9 +39,11 @@ __device__ __forceinline__ float act_value(float v, int act) {
 // an infinite one), GELU'(z) = Phi(z) + z phi(z).  The product is rounded by
 // itself, so that db's sums have the same bits whether or not dZ is stored.
 __device__ __forceinline__ float act_backward(float dy, float z, int act) {
-    if (act == kActGelu)
-        return __fmul_rn(dy, fmaf(z * 0.39894228040143267794f, expf(-0.5f * z * z),
-                                  0.5f * (1.0f + erff(z * 0.70710678118654752440f))));
+    if (act == kActGelu) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return __fmul_rn(dy, fmaf(z * 0.39894228040143267794f, e, c));
+    }
     if (act == kActRelu) return z > 0.0f ? dy : 0.0f;
     return dy;
 }
