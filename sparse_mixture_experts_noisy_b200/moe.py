@@ -6,7 +6,6 @@ built, or no CUDA device is present, the calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -386,19 +385,20 @@ def moe_load_stats(topk_idx, E, cf, gates=None, stream=None):
     return dict(load=load, used=used, importance=imp)
 
 
-_HERE = contextlib.nullcontext()
+_F32 = torch.float32
 
 
-def _placed(x, stream):
-    """Context in which a call's outputs are allocated and its kernels launched:
-    x's device, and `stream` (which must be of that device) or the current one."""
-    if stream is not None:
-        if stream.device != x.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-        return torch.cuda.stream(stream)
-    if x.get_device() != torch.cuda.current_device():
+def _elsewhere(x, stream):
+    """None when a call can run as it stands: no stream given, x on the current
+    device.  Otherwise the context in which its outputs are allocated and its
+    kernels launched: x's device, and `stream`, which must be of that device."""
+    if stream is None:
+        if x.get_device() == torch._C._cuda_getDevice():
+            return None
         return torch.cuda.device(x.device)
-    return _HERE
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    return torch.cuda.stream(stream)
 
 
 def _current(index):
@@ -417,17 +417,20 @@ def _arg(t, name, shape, dtype, index):
                      f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _scratch(ws, index):
-    """A caller's workspace (nullable) -> (pointer, bytes)."""
+def _scratch(ws, need, device, index):
+    """Scratch of `need` bytes: the caller's workspace, or a new one -> (pointer, bytes, what to keep alive)."""
     if ws is None:
-        return None, 0
+        if not need:
+            return None, 0, None
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), need, ws
     _cuda(ws, "ws")
     if ws.get_device() != index or ws.dtype is not torch.uint8:
         raise ValueError(f"ws must be uint8 on cuda:{index}, got {ws.dtype} on {ws.device}")
-    return ws.data_ptr(), ws.numel()
+    return ws.data_ptr(), ws.numel(), ws
 
 
-def _rows(x, name):
+def _matrix(x, name):
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(x.shape)}")
     _cuda(x, name)
@@ -439,28 +442,35 @@ def moe_layer_norm(x, gamma=None, beta=None, eps=1e-5, residual=None, want_stats
     """Layer norm of h = x + residual.  -> (y [N, d], h, mean [N] fp32, rstd [N] fp32).
     h is x without a residual and the stored sum with one (sum_out, which may
     be x or residual itself); mean and rstd are None unless want_stats."""
-    L = load_library()
-    N, d = _rows(x, "x")
-    dt, dev, at = _dt(x), x.device, x.get_device()
-    with _placed(x, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if residual is None:
-            h = x
-            if sum_out is not None:
-                raise ValueError("sum_out needs a residual")
+    shape = N, d = _matrix(x, "x")
+    if (at := _elsewhere(x, stream)) is not None:
+        with at:
+            return moe_layer_norm(x, gamma, beta, eps, residual, want_stats, y, sum_out)
+    L, dt, at, dtype = _lib or load_library(), _dt(x), x.get_device(), x.dtype
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _arg(y, "y", shape, dtype, at)
+    h, hp = x, None
+    if residual is not None:
+        if sum_out is None:
+            h = torch.empty_like(x)
+            hp = h.data_ptr()
         else:
-            h = sum_out = torch.empty_like(x) if sum_out is None else sum_out
-        mean = rstd = None
-        if want_stats:
-            mean = torch.empty(N, dtype=torch.float32, device=dev)
-            rstd = torch.empty(N, dtype=torch.float32, device=dev)
-        _check(L.moe_layer_norm(x.data_ptr(), _arg(residual, "residual", x.shape, x.dtype, at), dt,
-                                _arg(gamma, "gamma", (d,), torch.float32, at),
-                                _arg(beta, "beta", (d,), torch.float32, at), float(eps), N, d,
-                                _arg(y, "y", x.shape, x.dtype, at), _arg(sum_out, "sum_out", x.shape, x.dtype, at),
-                                mean.data_ptr() if want_stats else None, rstd.data_ptr() if want_stats else None,
-                                _current(at)))
+            h, hp = sum_out, _arg(sum_out, "sum_out", shape, dtype, at)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    mean = rstd = mp = rp = None
+    if want_stats:
+        mean = torch.empty(N, dtype=_F32, device=x.device)
+        rstd = torch.empty_like(mean)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    code = L.moe_layer_norm(x.data_ptr(), _arg(residual, "residual", shape, dtype, at), dt,
+                            _arg(gamma, "gamma", (d,), _F32, at), _arg(beta, "beta", (d,), _F32, at), eps, N, d, yp,
+                            hp, mp, rp, _current(at))
+    if code:
+        _check(code)
     return y, h, mean, rstd
 
 
@@ -469,28 +479,30 @@ def moe_layer_norm_backward(dy, h, mean, rstd, gamma=None, dres=None, want_param
     """Gradients of moe_layer_norm: h, mean and rstd are its outputs, dres the
     gradient that reaches h past the norm (nullable).
     -> dict(dx [N, d] of h's dtype, dgamma [d], dbeta [d] fp32, or None without want_params)."""
-    L = load_library()
-    N, d = _rows(h, "h")
-    dt, dev, at = _dt(h), h.device, h.get_device()
-    with _placed(h, stream):
-        if dx is None:
-            dx = torch.empty_like(h)
-        dg = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
-        db = torch.empty(d, dtype=torch.float32, device=dev) if want_params else None
-        if ws is None:
-            ws = torch.empty(L.moe_layer_norm_backward_workspace_size(N, d, dt), dtype=torch.uint8, device=dev)
-        wsp, wsn = _scratch(ws, at)
-        if mean is None or rstd is None:
-            raise ValueError("mean and rstd are needed (want_stats=True in the forward)")
-        _check(L.moe_layer_norm_backward(_arg(dy, "dy", h.shape, h.dtype, at), h.data_ptr(), dt,
-                                         _arg(gamma, "gamma", (d,), torch.float32, at),
-                                         _arg(mean, "mean", (N,), torch.float32, at),
-                                         _arg(rstd, "rstd", (N,), torch.float32, at),
-                                         _arg(dres, "dres", h.shape, h.dtype, at), N, d,
-                                         _arg(dx, "dx", h.shape, h.dtype, at),
-                                         dg.data_ptr() if want_params else None,
-                                         db.data_ptr() if want_params else None, wsp, wsn,
-                                         _current(at)))
+    shape = N, d = _matrix(h, "h")
+    if (at := _elsewhere(h, stream)) is not None:
+        with at:
+            return moe_layer_norm_backward(dy, h, mean, rstd, gamma, dres, want_params, dx, ws)
+    L, dt, at, dtype = _lib or load_library(), _dt(h), h.get_device(), h.dtype
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are needed (want_stats=True in the forward)")
+    if dx is None:
+        dx = torch.empty_like(h)
+        xp = dx.data_ptr()
+    else:
+        xp = _arg(dx, "dx", shape, dtype, at)
+    dg = db = gp = bp = None
+    if want_params:
+        dg = torch.empty(d, dtype=_F32, device=h.device)
+        db = torch.empty_like(dg)
+        gp, bp = dg.data_ptr(), db.data_ptr()
+    wp, wn, ws = _scratch(ws, L.moe_layer_norm_backward_workspace_size(N, d, dt), h.device, at)
+    code = L.moe_layer_norm_backward(_arg(dy, "dy", shape, dtype, at), h.data_ptr(), dt,
+                                     _arg(gamma, "gamma", (d,), _F32, at), _arg(mean, "mean", (N,), _F32, at),
+                                     _arg(rstd, "rstd", (N,), _F32, at), _arg(dres, "dres", shape, dtype, at), N, d,
+                                     xp, gp, bp, wp, wn, _current(at))
+    if code:
+        _check(code)
     return dict(dx=dx, dgamma=dg, dbeta=db)
 
 
@@ -498,24 +510,24 @@ def moe_linear(x, W, b=None, act=ACT_NONE, residual=None, keep_z=False, y=None, 
     """y = act(x W^T + b) + residual.  -> y [N, d_out], or (y, z) with keep_z (z
     the pre-activations, for moe_linear_backward).  x [N, d_in] and W [d_out,
     d_in] of one dtype, b [d_out] fp32; residual may be y itself."""
-    L = load_library()
-    N, d_in = _rows(x, "x")
-    d_out = _rows(W, "W")[0]
-    dt, dev, at = _dt(x), x.device, x.get_device()
-    with _placed(x, stream):
-        if y is None:
-            y = torch.empty((N, d_out), dtype=x.dtype, device=dev)
-        z = torch.empty((N, d_out), dtype=x.dtype, device=dev) if keep_z else None
-        need = L.moe_linear_workspace_size(N, d_in, d_out, dt)
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _scratch(ws, at)
-        _check(L.moe_linear(x.data_ptr(), dt, _arg(W, "W", (d_out, d_in), x.dtype, at),
-                            _arg(b, "b", (d_out,), torch.float32, at), int(act),
-                            _arg(residual, "residual", (N, d_out), x.dtype, at), N, d_in, d_out,
-                            _arg(y, "y", (N, d_out), x.dtype, at), z.data_ptr() if keep_z else None,
-                            wsp, wsn,
-                            _current(at)))
+    N, d_in = _matrix(x, "x")
+    d_out = _matrix(W, "W")[0]
+    if (at := _elsewhere(x, stream)) is not None:
+        with at:
+            return moe_linear(x, W, b, act, residual, keep_z, y, ws)
+    L, dt, at, dtype, out = _lib or load_library(), _dt(x), x.get_device(), x.dtype, (N, d_out)
+    if y is None:
+        y = torch.empty(out, dtype=dtype, device=x.device)
+        yp = y.data_ptr()
+    else:
+        yp = _arg(y, "y", out, dtype, at)
+    z = torch.empty_like(y) if keep_z else None
+    wp, wn, ws = _scratch(ws, L.moe_linear_workspace_size(N, d_in, d_out, dt), x.device, at)
+    code = L.moe_linear(x.data_ptr(), dt, _arg(W, "W", (d_out, d_in), dtype, at), _arg(b, "b", (d_out,), _F32, at),
+                        act, _arg(residual, "residual", out, dtype, at), N, d_in, d_out, yp,
+                        z.data_ptr() if keep_z else None, wp, wn, _current(at))
+    if code:
+        _check(code)
     return (y, z) if keep_z else y
 
 
@@ -524,25 +536,22 @@ def moe_linear_backward(dy, x, W, act=ACT_NONE, z=None, want_dx=True, want_dW=Tr
     """Gradients of moe_linear (the residual's is dy).  z: the forward's
     pre-activations (keep_z), needed unless act is ACT_NONE.
     -> dict(dx [N, d_in] of x's dtype, dW [d_out, d_in] of W's dtype, db [d_out] fp32; None where not wanted)."""
-    L = load_library()
-    N, d_in = _rows(x, "x")
-    d_out = _rows(W, "W")[0]
-    dt, dev, at = _dt(x), x.device, x.get_device()
-    with _placed(x, stream):
-        dx = torch.empty_like(x) if want_dx else None
-        dW = torch.empty_like(W) if want_dW else None
-        db = torch.empty(d_out, dtype=torch.float32, device=dev) if want_db else None
-        need = L.moe_linear_backward_workspace_size(N, d_in, d_out, int(act), dt)
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _scratch(ws, at)
-        _check(L.moe_linear_backward(_arg(dy, "dy", (N, d_out), x.dtype, at), x.data_ptr(), dt,
-                                     _arg(W, "W", (d_out, d_in), x.dtype, at),
-                                     _arg(z, "z", (N, d_out), x.dtype, at), int(act), N, d_in, d_out,
-                                     dx.data_ptr() if want_dx else None, dW.data_ptr() if want_dW else None,
-                                     db.data_ptr() if want_db else None,
-                                     wsp, wsn,
-                                     _current(at)))
+    N, d_in = _matrix(x, "x")
+    d_out = _matrix(W, "W")[0]
+    if (at := _elsewhere(x, stream)) is not None:
+        with at:
+            return moe_linear_backward(dy, x, W, act, z, want_dx, want_dW, want_db, ws)
+    L, dt, at, dtype, out = _lib or load_library(), _dt(x), x.get_device(), x.dtype, (N, d_out)
+    dx = torch.empty_like(x) if want_dx else None
+    dW = torch.empty_like(W) if want_dW else None
+    db = torch.empty(d_out, dtype=_F32, device=x.device) if want_db else None
+    wp, wn, ws = _scratch(ws, L.moe_linear_backward_workspace_size(N, d_in, d_out, act, dt), x.device, at)
+    code = L.moe_linear_backward(_arg(dy, "dy", out, dtype, at), x.data_ptr(), dt,
+                                 _arg(W, "W", (d_out, d_in), dtype, at), _arg(z, "z", out, dtype, at), act, N, d_in,
+                                 d_out, dx.data_ptr() if want_dx else None, dW.data_ptr() if want_dW else None,
+                                 db.data_ptr() if want_db else None, wp, wn, _current(at))
+    if code:
+        _check(code)
     return dict(dx=dx, dW=dW, db=db)
 
 
