@@ -67,6 +67,40 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64
     return true;
 }
 
+// One lane of a converged warp.  The TMA and MMA warps run their loops whole and
+// let this lane issue: the loop's state then stays in uniform registers.  With
+// the loop inside `if (lane == 0)`, and operand layouts tested per K block, a
+// stage cost the issuing thread about 400 ns, more than its MMAs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// mbar_wait_bounded by a whole converged warp, every lane polling.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t *status, uint64_t timeout_ns,
+                                          uint32_t where) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status, timeout_ns, where));
+}
+
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+// f(operand P is MN-major, operand Q is MN-major) with the layouts as constants.
+template <typename F> __device__ __forceinline__ void by_layout(const bool p_mn, const bool q_mn, F f) {
+    if (!p_mn) f(No{}, No{});
+    else if (!q_mn) f(Yes{}, No{});
+    else f(Yes{}, Yes{});
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -244,118 +278,130 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const uint64_t pol = policy_evict_normal();
-            PairUnit t;
-            for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
-                const ProdArgs &p = args.p[t.prob];
-                const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
-                const int nr = t.n0 + static_cast<int>(rank) * 128;
-                const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * QR;
-                for (int kb = 0; kb < p.kb; ++kb) {
-                    if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 61)) {
+        const bool one = elect_one();
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint64_t pol = policy_evict_normal();
+        PairUnit t;
+        for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
+            const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
+            const int nr = t.n0 + static_cast<int>(rank) * 128;
+            const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * QR;
+            const int kbs = args.p[t.prob].kb;
+            by_layout(args.p[t.prob].p_mn != 0, args.p[t.prob].q_mn != 0, [&](auto pm, auto qm) {
+                for (int kb = 0; kb < kbs; ++kb) {
+                    if (!wait_warp(empty0 + 8 * stage, phase ^ 1u, status, tmo, 61)) {
                         ok = false;
                         break;
                     }
-                    if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
-                    const uint32_t fb = full0_lead + 8 * stage;
-                    const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                    const int kx = kb * kBK;
+                    if (one) {
+                        const uint32_t fb = full0_lead + 8 * stage;
+                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                        const int kx = kb * kBK;
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
 #pragma unroll
-                    for (int z = 0; z < PLANES; ++z) {
-                        const uint32_t a = sa + z * P_BYTES, b = sa + Q_AT + z * Q_BYTES;
-                        if (p.p_mn) {
-                            tma_load_3d_pair(a, tp, fb, nr, kx, z, pol);
-                            tma_load_3d_pair(a + 8192u, tp, fb, nr + 64, kx, z, pol);
-                        } else {
-                            tma_load_3d_pair(a, tp, fb, kx, nr, z, pol);
-                        }
-                        if (p.q_mn) {
-                            tma_load_3d_pair(b, tq, fb, mr, kx, z, pol);
-                            if constexpr (QR == 128) tma_load_3d_pair(b + 8192u, tq, fb, mr + 64, kx, z, pol);
-                        } else {
-                            tma_load_3d_pair(b, tq, fb, kx, mr, z, pol);
+                        for (int z = 0; z < PLANES; ++z) {
+                            const uint32_t a = sa + z * P_BYTES, b = sa + Q_AT + z * Q_BYTES;
+                            if constexpr (decltype(pm)::value) {
+                                tma_load_3d_pair(a, tp, fb, nr, kx, z, pol);
+                                tma_load_3d_pair(a + 8192u, tp, fb, nr + 64, kx, z, pol);
+                            } else {
+                                tma_load_3d_pair(a, tp, fb, kx, nr, z, pol);
+                            }
+                            if constexpr (decltype(qm)::value) {
+                                tma_load_3d_pair(b, tq, fb, mr, kx, z, pol);
+                                if constexpr (QR == 128) tma_load_3d_pair(b + 8192u, tq, fb, mr + 64, kx, z, pol);
+                            } else {
+                                tma_load_3d_pair(b, tq, fb, kx, mr, z, pol);
+                            }
                         }
                     }
+                    __syncwarp();
                     ++issued;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-            }
-            if (!ok && leader) {
-                // the pair's copies of the stages armed here land before exit
-                int st = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < STAGES && i < issued; ++i) {
-                    if (st == 0) {
-                        st = STAGES - 1;
-                        ph ^= 1u;
-                    } else {
-                        --st;
-                    }
-                    wait_drain(full0 + 8 * st, ph, tmo);
+            });
+        }
+        if (!ok && leader && one) {
+            // the pair's copies of the stages armed here land before exit
+            int st = stage;
+            uint32_t ph = phase;
+            for (int i = 0; i < STAGES && i < issued; ++i) {
+                if (st == 0) {
+                    st = STAGES - 1;
+                    ph ^= 1u;
+                } else {
+                    --st;
                 }
+                wait_drain(full0 + 8 * st, ph, tmo);
             }
         }
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        if (leader) {
+            const bool one = elect_one();
             int stage = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true, any = false;
             PairUnit t;
             for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
-                const ProdArgs &p = args.p[t.prob];
-                const bool pm = p.p_mn != 0, qm = p.q_mn != 0;
-                const uint32_t idesc = idesc_bf16_f32(256, TM) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
-                // K-major: the next 16 of K are 32 bytes on in the swizzled row;
-                // MN-major: 16 rows of 128 bytes on
-                const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
-                const int piece = SPLIT ? kPieceKb : p.kb;
-                for (int k0 = 0; k0 < p.kb && ok; k0 += piece) {
-                    const int n = k0 + piece < p.kb ? piece : p.kb - k0;
-                    const int acc = local & 1;
-                    if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 62)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TM);
-                    for (int k = 0; k < n; ++k) {
-                        if (!mbar_wait_bounded(full0 + 8 * stage, phase, status, tmo, 63)) {
+                const int kbs = args.p[t.prob].kb;
+                by_layout(args.p[t.prob].p_mn != 0, args.p[t.prob].q_mn != 0, [&](auto pm, auto qm) {
+                    constexpr bool PM = decltype(pm)::value, QM = decltype(qm)::value;
+                    constexpr uint32_t idesc = idesc_bf16_f32(256, TM) | (PM ? kIdescAMajorMN : 0u) | (QM ? kIdescBMajorMN : 0u);
+                    // K-major: the next 16 of K are 32 bytes on in the swizzled row;
+                    // MN-major: 16 rows of 128 bytes on
+                    constexpr uint32_t astep = PM ? 128u : 2u, bstep = QM ? 128u : 2u;
+                    const int piece = SPLIT ? kPieceKb : kbs;
+                    for (int k0 = 0; k0 < kbs && ok; k0 += piece) {
+                        const int n = k0 + piece < kbs ? piece : kbs - k0;
+                        const int acc = local & 1;
+                        if (!wait_warp(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 62)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                        const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
-                        const uint64_t bd = qm ? smem_desc_mn_sw128(sa + Q_AT, 8192u, 1024u) : smem_desc_sw128(sa + Q_AT);
+                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TM);
+                        for (int k = 0; k < n; ++k) {
+                            if (!wait_warp(full0 + 8 * stage, phase, status, tmo, 63)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            if (one) {
+                                const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                                const uint64_t ad = PM ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
+                                const uint64_t bd = QM ? smem_desc_mn_sw128(sa + Q_AT, 8192u, 1024u)
+                                                       : smem_desc_sw128(sa + Q_AT);
 #pragma unroll
-                        for (int x = 0; x < TERMS; ++x) {
-                            const uint64_t ax = ad + (SPLIT ? term_p(x) * (P_BYTES >> 4) : 0);
-                            const uint64_t bx = bd + (SPLIT ? term_q(x) * (Q_BYTES >> 4) : 0);
+                                for (int x = 0; x < TERMS; ++x) {
+                                    const uint64_t ax = ad + (SPLIT ? term_p(x) * (P_BYTES >> 4) : 0);
+                                    const uint64_t bx = bd + (SPLIT ? term_q(x) * (Q_BYTES >> 4) : 0);
 #pragma unroll
-                            for (int kk = 0; kk < kBK / 16; ++kk)
-                                umma_bf16_pair(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
-                                               (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                                    for (int kk = 0; kk < kBK / 16; ++kk)
+                                        umma_bf16_pair(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                                       (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                                }
+                                umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                            }
+                            __syncwarp();
+                            any = true;
+                            if (++stage == STAGES) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
                         }
-                        any = true;
-                        umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                        if (!ok) break;
+                        if (one) umma_commit_pair_mc(tfull0 + 8 * acc, 0x3);
+                        __syncwarp();
+                        ++local;
                     }
-                    if (!ok) break;
-                    umma_commit_pair_mc(tfull0 + 8 * acc, 0x3);
-                    ++local;
-                }
+                });
             }
-            if (!ok && any) {
+            if (!ok && any && one) {
                 umma_commit_pair(drain);
                 wait_drain(drain, 0, tmo);
             }
@@ -508,103 +554,112 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
     float sum[BN];
     bool good = true;
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
+        const bool one = elect_one();
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        by_layout(p.p_mn != 0, p.q_mn != 0, [&](auto pm, auto qm) {
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, status, tmo, 71)) {
+                if (!wait_warp(empty0 + 8 * stage, phase ^ 1u, status, tmo, 71)) {
                     ok = false;
                     break;
                 }
-                const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
-                mbar_arrive_expect_tx(fb, stage_bytes);
-                const int kx = kb * kBK, mr = static_cast<int>(m0);
+                if (one) {
+                    const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
+                    mbar_arrive_expect_tx(fb, stage_bytes);
+                    const int kx = kb * kBK, mr = static_cast<int>(m0);
 #pragma unroll
-                for (int z = 0; z < PLANES; ++z) {
-                    const uint32_t a = sa + z * A_BYTES, b = sa + PLANES * A_BYTES + z * b_bytes;
-                    if (p.p_mn) {
-                        tma_load_3d(a, &tp, fb, n0, kx, z);
-                        tma_load_3d(a + 8192u, &tp, fb, n0 + 64, kx, z);
-                    } else {
-                        tma_load_3d(a, &tp, fb, kx, n0, z);
-                    }
-                    if (p.q_mn) {
-                        tma_load_3d(b, &tq, fb, mr, kx, z);
-                        if constexpr (BN == 128) tma_load_3d(b + 8192u, &tq, fb, mr + 64, kx, z);
-                    } else {
-                        tma_load_3d(b, &tq, fb, kx, mr, z);
+                    for (int z = 0; z < PLANES; ++z) {
+                        const uint32_t a = sa + z * A_BYTES, b = sa + PLANES * A_BYTES + z * b_bytes;
+                        if constexpr (decltype(pm)::value) {
+                            tma_load_3d(a, &tp, fb, n0, kx, z);
+                            tma_load_3d(a + 8192u, &tp, fb, n0 + 64, kx, z);
+                        } else {
+                            tma_load_3d(a, &tp, fb, kx, n0, z);
+                        }
+                        if constexpr (decltype(qm)::value) {
+                            tma_load_3d(b, &tq, fb, mr, kx, z);
+                            if constexpr (BN == 128) tma_load_3d(b + 8192u, &tq, fb, mr + 64, kx, z);
+                        } else {
+                            tma_load_3d(b, &tq, fb, kx, mr, z);
+                        }
                     }
                 }
+                __syncwarp();
                 ++issued;
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
-            if (!ok) {
-                int st = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < stages && i < issued; ++i) {
-                    if (st == 0) {
-                        st = stages - 1;
-                        ph ^= 1u;
-                    } else {
-                        --st;
-                    }
-                    wait_drain(full0 + 8 * st, ph, tmo);
+        });
+        if (!ok && one) {
+            int st = stage;
+            uint32_t ph = phase;
+            for (int i = 0; i < stages && i < issued; ++i) {
+                if (st == 0) {
+                    st = stages - 1;
+                    ph ^= 1u;
+                } else {
+                    --st;
                 }
+                wait_drain(full0 + 8 * st, ph, tmo);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, local = 0;
-            uint32_t phase = 0;
-            bool ok = true, any = false;
-            const bool pm = p.p_mn != 0, qm = p.q_mn != 0;
-            const uint32_t idesc = idesc_bf16_f32(128, BN) | (pm ? kIdescAMajorMN : 0u) | (qm ? kIdescBMajorMN : 0u);
-            const uint32_t astep = pm ? 128u : 2u, bstep = qm ? 128u : 2u;
+        const bool one = elect_one();
+        int stage = 0, local = 0;
+        uint32_t phase = 0;
+        bool ok = true, any = false;
+        by_layout(p.p_mn != 0, p.q_mn != 0, [&](auto pm, auto qm) {
+            constexpr bool PM = decltype(pm)::value, QM = decltype(qm)::value;
+            constexpr uint32_t idesc = idesc_bf16_f32(128, BN) | (PM ? kIdescAMajorMN : 0u) | (QM ? kIdescBMajorMN : 0u);
+            constexpr uint32_t astep = PM ? 128u : 2u, bstep = QM ? 128u : 2u;
             for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++local) {
                 const int n = k0 + piece < kb1 ? piece : kb1 - k0;
                 const int acc = local & 1;
-                if (!mbar_wait_bounded(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 72)) {
+                if (!wait_warp(tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, status, tmo, 72)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * COLS);
                 for (int k = 0; k < n; ++k) {
-                    if (!mbar_wait_bounded(full0 + 8 * stage, phase, status, tmo, 73)) {
+                    if (!wait_warp(full0 + 8 * stage, phase, status, tmo, 73)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_base + stage * stage_bytes;
-                    const uint32_t sb = sa + PLANES * A_BYTES;
-                    const uint64_t ad = pm ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
-                    const uint64_t bd = qm ? smem_desc_mn_sw128(sb, 8192u, 1024u) : smem_desc_sw128(sb);
+                    if (one) {
+                        const uint32_t sa = smem_base + stage * stage_bytes;
+                        const uint32_t sb = sa + PLANES * A_BYTES;
+                        const uint64_t ad = PM ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
+                        const uint64_t bd = QM ? smem_desc_mn_sw128(sb, 8192u, 1024u) : smem_desc_sw128(sb);
 #pragma unroll
-                    for (int x = 0; x < TERMS; ++x) {
-                        const uint64_t ax = ad + (SPLIT ? term_p(x) * (A_BYTES >> 4) : 0);
-                        const uint64_t bx = bd + (SPLIT ? term_q(x) * (b_bytes >> 4) : 0);
+                        for (int x = 0; x < TERMS; ++x) {
+                            const uint64_t ax = ad + (SPLIT ? term_p(x) * (A_BYTES >> 4) : 0);
+                            const uint64_t bx = bd + (SPLIT ? term_q(x) * (b_bytes >> 4) : 0);
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            umma_bf16(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
-                                      (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < kBK / 16; ++kk)
+                                umma_bf16(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                          (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        umma_commit(empty0 + 8 * stage);
                     }
+                    __syncwarp();
                     any = true;
-                    umma_commit(empty0 + 8 * stage);
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) umma_commit(tfull0 + 8 * acc);
+                if (ok && one) umma_commit(tfull0 + 8 * acc);
+                __syncwarp();
             }
-            if (!ok && any) {
-                umma_commit(drain);
-                wait_drain(drain, 0, tmo);
-            }
+        });
+        if (!ok && any && one) {
+            umma_commit(drain);
+            wait_drain(drain, 0, tmo);
         }
     } else {
         const int q = warp & 3;
