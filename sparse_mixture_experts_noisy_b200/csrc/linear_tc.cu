@@ -54,9 +54,10 @@ __device__ __forceinline__ int term_p(int t) { return t == 1 ? 2 : (t == 2 || t 
 __device__ __forceinline__ int term_q(int t) { return t == 0 ? 2 : (t == 2 || t == 3) ? 1 : 0; }
 
 struct ProdArgs {
-    int64_t M;      // rows of D
-    int Nn, kb;     // columns of D, K blocks
-    int p_mn, q_mn; // operand stored with k as its rows
+    int64_t M;       // rows of D
+    int Nn, kb;      // columns of D, K blocks
+    int p_mn, q_mn;  // operand stored with k as its rows
+    int tm;          // pairs: rows of D in a tile
     LinearEpi epi;
 };
 
@@ -71,14 +72,72 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64
 // let this lane issue: the loop's state then stays in uniform registers.  With
 // the loop inside `if (lane == 0)`, and operand layouts tested per K block, a
 // stage cost the issuing thread about 400 ns, more than its MMAs.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(p));
-    return p != 0;
+    return p;
+}
+
+// The issuing instructions, executed by the lanes with `one` set.  As predicated
+// instructions in converged code, not under a branch: addresses and descriptors
+// are then computed in uniform registers.
+__device__ __forceinline__ void expect_tx_if(uint32_t one, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_if(uint32_t one, uint32_t dst, const void *tmap, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_pair_if(uint32_t one, uint32_t dst, const void *tmap, uint32_t bar, int x, int y,
+                                             int z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(one)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+            : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit_both_if(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(bar), "h"(static_cast<uint16_t>(3)), "r"(one)
+        : "memory");
 }
 
 // mbar_wait_bounded by a whole converged warp, every lane polling.
@@ -161,11 +220,11 @@ __device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc,
 }
 
 // ---------------------------------------------------------------- CTA pairs
-// A pair of CTAs (tcgen05 cta_group::2) computes 256 x 256 tiles of D: CTA r
-// loads P rows [n0 + 128 r, +128) and Q rows [m0 + 128 r, +128) per K block, the
-// leader's MMA reads both, and each CTA's tensor memory gets its 128 n of all
-// 256 m.  fp32 tiles are 256 n x 128 m: an epilogue thread then adds 64 columns in
-// registers, and six products per load keep L2 traffic low all the same.
+// A pair of CTAs (tcgen05 cta_group::2) computes tiles of 256 n x tm m of D, tm
+// 128, 192 or 256: CTA r loads P rows [n0 + 128 r, +128) and Q rows
+// [m0 + r tm / 2, + tm / 2) per K block, the leader's MMA reads both, and each
+// CTA's tensor memory gets its 128 n of all tm m.  fp32 tiles have 192 m at most,
+// of which an epilogue thread adds 96 columns in registers.
 // Persistent, one pair per two SMs; two accumulators, so the epilogue of
 // one tile (or piece) overlaps the MMAs of the next.  Warp 0: TMA; warp 1: MMA;
 // warps 2-9: epilogue, two groups of four, each half of the m.
@@ -175,15 +234,20 @@ __device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc,
 // with the pairs that got one fewer of the first's, as many as fit into the time
 // the others still need, before they are dealt to all.
 constexpr int kPairThreads = 320;
-constexpr int pair_tile_m(bool fp32) { return fp32 ? 128 : 256; }
-constexpr int pair_stages(bool fp32) { return fp32 ? 3 : 6; }
-constexpr int pair_stage_bytes(bool fp32) { return fp32 ? 3 * (128 + 64) * kBK * 2 : (128 + 128) * kBK * 2; }
+constexpr int kPairMaxStages = 6;
+constexpr int kPairRing = 216 * 1024;
+constexpr int pair_max_tm(bool fp32) { return fp32 ? 192 : 256; }
+// Bytes of a CTA's Q rows in a plane of a stage: 64-wide boxes when MN-major.
+__host__ __device__ constexpr int pair_q_bytes(int tm, bool mn) {
+    return (mn ? (tm / 2 + 63) / 64 * 64 : tm / 2) * kBK * 2;
+}
 constexpr int kGroupM = 8;  // m tiles that share a sweep over n: their Q rows stay in L2
 
 struct PairArgs {
     ProdArgs p[2];
     int units[2];
     int late, early;  // second product: pairs [0, late) start late; the others do `early` units first
+    int stages, q_room;  // ring slots; bytes a slot keeps for a plane of Q
     uint64_t timeout_ns;
 };
 
@@ -192,7 +256,6 @@ struct PairUnit {
     int64_t m0;
 };
 
-template <int TM>
 __device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npairs, int i, PairUnit &t) {
     const int n1 = pair < a.units[0] ? (a.units[0] - pair + npairs - 1) / npairs : 0;
     int u;
@@ -211,11 +274,11 @@ __device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npair
         if (u >= a.units[1]) return false;
     }
     const ProdArgs &p = a.p[t.prob];
-    const int mt = static_cast<int>((p.M + TM - 1) / TM), nt = (p.Nn + 255) / 256;
+    const int mt = static_cast<int>((p.M + p.tm - 1) / p.tm), nt = (p.Nn + 255) / 256;
     const int sweep = kGroupM * nt;
     const int grp = u / sweep, rem = u - grp * sweep;
     const int rows = mt - grp * kGroupM < kGroupM ? mt - grp * kGroupM : kGroupM;
-    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * TM;
+    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * p.tm;
     t.n0 = rem / rows * 256;
     return true;
 }
@@ -227,14 +290,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                    const __grid_constant__ PairArgs args) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
-    constexpr int TM = pair_tile_m(SPLIT), QR = TM / 2, HALF = TM / 2;  // Q rows a CTA; m an epilogue group
-    constexpr int STAGES = pair_stages(SPLIT);
-    constexpr uint32_t P_BYTES = 128 * kBK * 2, Q_BYTES = QR * kBK * 2, Q_AT = PLANES * P_BYTES;
-    constexpr uint32_t STAGE_BYTES = pair_stage_bytes(SPLIT);
-    static_assert(STAGE_BYTES == PLANES * (P_BYTES + Q_BYTES) && STAGE_BYTES % 1024 == 0, "stage");
+    constexpr int HMAX = pair_max_tm(SPLIT) / 2;
+    constexpr uint32_t P_BYTES = 128 * kBK * 2, Q_AT = PLANES * P_BYTES;
+    const int stages = args.stages;
+    const uint32_t q_room = args.q_room, stage_bytes = PLANES * (P_BYTES + q_room);
 
     extern __shared__ uint8_t dyn_smem[];
-    __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kPairMaxStages + 5];
     __shared__ uint32_t tmem_holder;
     __shared__ uint32_t cta_status;
 
@@ -245,14 +307,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     uint32_t *status = &cta_status;
     const uint64_t tmo = args.timeout_ns;
     const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
-    const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
-    const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
-    const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]);
+    const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kPairMaxStages]);
+    const uint32_t tfull0 = smem_u32(&bars[2 * kPairMaxStages]), tempty0 = smem_u32(&bars[2 * kPairMaxStages + 2]);
+    const uint32_t drain = smem_u32(&bars[2 * kPairMaxStages + 4]);
     const uint32_t full0_lead = map_to_cta(full0, 0), tempty0_lead = map_to_cta(tempty0, 0);
 
     pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
@@ -278,16 +340,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     pdl_wait();
 
     if (warp == 0) {
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint64_t pol = policy_evict_normal();
         PairUnit t;
-        for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
+        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
             const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
             const int nr = t.n0 + static_cast<int>(rank) * 128;
-            const int mr = static_cast<int>(t.m0) + static_cast<int>(rank) * QR;
+            const int qr = args.p[t.prob].tm / 2, mr = static_cast<int>(t.m0) + static_cast<int>(rank) * qr;
             const int kbs = args.p[t.prob].kb;
             by_layout(args.p[t.prob].p_mn != 0, args.p[t.prob].q_mn != 0, [&](auto pm, auto qm) {
                 for (int kb = 0; kb < kbs; ++kb) {
@@ -295,31 +356,32 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                         ok = false;
                         break;
                     }
-                    if (one) {
-                        const uint32_t fb = full0_lead + 8 * stage;
-                        const uint32_t sa = smem_base + stage * STAGE_BYTES;
-                        const int kx = kb * kBK;
-                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+                    const uint32_t fb = full0_lead + 8 * stage;
+                    const uint32_t sa = smem_base + stage * stage_bytes;
+                    const int kx = kb * kBK;
+                    expect_tx_if(leader ? one : 0u, full0 + 8 * stage,
+                                 2 * PLANES * (P_BYTES + pair_q_bytes(2 * qr, decltype(qm)::value)));
+                    {
 #pragma unroll
                         for (int z = 0; z < PLANES; ++z) {
-                            const uint32_t a = sa + z * P_BYTES, b = sa + Q_AT + z * Q_BYTES;
+                            const uint32_t a = sa + z * P_BYTES, b = sa + Q_AT + z * q_room;
                             if constexpr (decltype(pm)::value) {
-                                tma_load_3d_pair(a, tp, fb, nr, kx, z, pol);
-                                tma_load_3d_pair(a + 8192u, tp, fb, nr + 64, kx, z, pol);
+                                load_pair_if(one, a, tp, fb, nr, kx, z);
+                                load_pair_if(one, a + 8192u, tp, fb, nr + 64, kx, z);
                             } else {
-                                tma_load_3d_pair(a, tp, fb, kx, nr, z, pol);
+                                load_pair_if(one, a, tp, fb, kx, nr, z);
                             }
                             if constexpr (decltype(qm)::value) {
-                                tma_load_3d_pair(b, tq, fb, mr, kx, z, pol);
-                                if constexpr (QR == 128) tma_load_3d_pair(b + 8192u, tq, fb, mr + 64, kx, z, pol);
+                                load_pair_if(one, b, tq, fb, mr, kx, z);
+                                if (qr > 64) load_pair_if(one, b + 8192u, tq, fb, mr + 64, kx, z);
                             } else {
-                                tma_load_3d_pair(b, tq, fb, kx, mr, z, pol);
+                                load_pair_if(one, b, tq, fb, kx, mr, z);
                             }
                         }
                     }
                     __syncwarp();
                     ++issued;
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -330,9 +392,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             // the pair's copies of the stages armed here land before exit
             int st = stage;
             uint32_t ph = phase;
-            for (int i = 0; i < STAGES && i < issued; ++i) {
+            for (int i = 0; i < stages && i < issued; ++i) {
                 if (st == 0) {
-                    st = STAGES - 1;
+                    st = stages - 1;
                     ph ^= 1u;
                 } else {
                     --st;
@@ -342,16 +404,17 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         }
     } else if (warp == 1) {
         if (leader) {
-            const bool one = elect_one();
+            const uint32_t one = elect_one();
             int stage = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true, any = false;
             PairUnit t;
-            for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
+            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
                 const int kbs = args.p[t.prob].kb;
                 by_layout(args.p[t.prob].p_mn != 0, args.p[t.prob].q_mn != 0, [&](auto pm, auto qm) {
                     constexpr bool PM = decltype(pm)::value, QM = decltype(qm)::value;
-                    constexpr uint32_t idesc = idesc_bf16_f32(256, TM) | (PM ? kIdescAMajorMN : 0u) | (QM ? kIdescBMajorMN : 0u);
+                    const uint32_t idesc = idesc_bf16_f32(256, args.p[t.prob].tm) | (PM ? kIdescAMajorMN : 0u) |
+                                           (QM ? kIdescBMajorMN : 0u);
                     // K-major: the next 16 of K are 32 bytes on in the swizzled row;
                     // MN-major: 16 rows of 128 bytes on
                     constexpr uint32_t astep = PM ? 128u : 2u, bstep = QM ? 128u : 2u;
@@ -364,38 +427,38 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TM);
+                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
                         for (int k = 0; k < n; ++k) {
                             if (!wait_warp(full0 + 8 * stage, phase, status, tmo, 63)) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
-                            if (one) {
-                                const uint32_t sa = smem_base + stage * STAGE_BYTES;
+                            {
+                                const uint32_t sa = smem_base + stage * stage_bytes;
                                 const uint64_t ad = PM ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
                                 const uint64_t bd = QM ? smem_desc_mn_sw128(sa + Q_AT, 8192u, 1024u)
                                                        : smem_desc_sw128(sa + Q_AT);
 #pragma unroll
                                 for (int x = 0; x < TERMS; ++x) {
                                     const uint64_t ax = ad + (SPLIT ? term_p(x) * (P_BYTES >> 4) : 0);
-                                    const uint64_t bx = bd + (SPLIT ? term_q(x) * (Q_BYTES >> 4) : 0);
+                                    const uint64_t bx = bd + (SPLIT ? term_q(x) * (q_room >> 4) : 0);
 #pragma unroll
                                     for (int kk = 0; kk < kBK / 16; ++kk)
-                                        umma_bf16_pair(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                        mma_if<true>(one, d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
                                                        (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
                                 }
-                                umma_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                                commit_both_if(one, empty0 + 8 * stage);
                             }
                             __syncwarp();
                             any = true;
-                            if (++stage == STAGES) {
+                            if (++stage == stages) {
                                 stage = 0;
                                 phase ^= 1u;
                             }
                         }
                         if (!ok) break;
-                        if (one) umma_commit_pair_mc(tfull0 + 8 * acc, 0x3);
+                        commit_both_if(one, tfull0 + 8 * acc);
                         __syncwarp();
                         ++local;
                     }
@@ -411,14 +474,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         int local = 0;
         bool ok = true;
         PairUnit t;
-        for (int i = 0; ok && pair_unit<TM>(args, pair, npairs, i, t); ++i) {
+        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
             const ProdArgs &p = args.p[t.prob];
             const int n = t.n0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-            const int64_t m0 = t.m0 + half * HALF;
+            const int hm = p.tm / 2;  // m of this group
+            const int64_t m0 = t.m0 + half * hm;
             const int64_t left = p.M - m0;
-            const int rows = left < HALF ? static_cast<int>(left > 0 ? left : 0) : HALF;
+            const int rows = left < hm ? static_cast<int>(left > 0 ? left : 0) : hm;
             const float bias = (FULL && p.epi.bias != nullptr && n < p.Nn) ? p.epi.bias[n] : 0.0f;
-            float sum[SPLIT ? HALF : 1];
+            float sum[SPLIT ? HMAX : 1];
             const int pieces = SPLIT ? (p.kb + kPieceKb - 1) / kPieceKb : 1;
             for (int pc = 0; pc < pieces; ++pc) {
                 const int acc = local & 1;
@@ -428,10 +492,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                 }
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                       static_cast<uint32_t>(acc * TM + half * HALF);
+                                       static_cast<uint32_t>(acc * 256 + half * hm);
                 if constexpr (SPLIT) {
 #pragma unroll
-                    for (int c = 0; c < HALF / 16; ++c) {
+                    for (int c = 0; c < HMAX / 16; ++c) {
+                        if (c * 16 >= hm) break;
                         uint32_t r[16];
                         tmem_ld_32x32b_x16(taddr + c * 16, r);
                         tmem_wait_ld();
@@ -460,7 +525,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             if constexpr (SPLIT) {
                 if (ok && n < p.Nn) {
 #pragma unroll
-                    for (int c = 0; c < HALF / 16; ++c)
+                    for (int c = 0; c < HMAX / 16; ++c)
                         if (c * 16 < rows)
                             store_cols<T, FULL, 16>(p.epi, sum + c * 16, m0 + c * 16, n, p.Nn, rows - c * 16, bias);
                 }
@@ -554,7 +619,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
     float sum[BN];
     bool good = true;
     if (warp == 0) {
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -564,24 +629,24 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                     ok = false;
                     break;
                 }
-                if (one) {
+                {
                     const uint32_t fb = full0 + 8 * stage, sa = smem_base + stage * stage_bytes;
-                    mbar_arrive_expect_tx(fb, stage_bytes);
+                    expect_tx_if(one, fb, stage_bytes);
                     const int kx = kb * kBK, mr = static_cast<int>(m0);
 #pragma unroll
                     for (int z = 0; z < PLANES; ++z) {
                         const uint32_t a = sa + z * A_BYTES, b = sa + PLANES * A_BYTES + z * b_bytes;
                         if constexpr (decltype(pm)::value) {
-                            tma_load_3d(a, &tp, fb, n0, kx, z);
-                            tma_load_3d(a + 8192u, &tp, fb, n0 + 64, kx, z);
+                            load_if(one, a, &tp, fb, n0, kx, z);
+                            load_if(one, a + 8192u, &tp, fb, n0 + 64, kx, z);
                         } else {
-                            tma_load_3d(a, &tp, fb, kx, n0, z);
+                            load_if(one, a, &tp, fb, kx, n0, z);
                         }
                         if constexpr (decltype(qm)::value) {
-                            tma_load_3d(b, &tq, fb, mr, kx, z);
-                            if constexpr (BN == 128) tma_load_3d(b + 8192u, &tq, fb, mr + 64, kx, z);
+                            load_if(one, b, &tq, fb, mr, kx, z);
+                            if constexpr (BN == 128) load_if(one, b + 8192u, &tq, fb, mr + 64, kx, z);
                         } else {
-                            tma_load_3d(b, &tq, fb, kx, mr, z);
+                            load_if(one, b, &tq, fb, kx, mr, z);
                         }
                     }
                 }
@@ -607,7 +672,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
             }
         }
     } else if (warp == 1) {
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         int stage = 0, local = 0;
         uint32_t phase = 0;
         bool ok = true, any = false;
@@ -630,7 +695,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                         break;
                     }
                     tc_fence_after();
-                    if (one) {
+                    {
                         const uint32_t sa = smem_base + stage * stage_bytes;
                         const uint32_t sb = sa + PLANES * A_BYTES;
                         const uint64_t ad = PM ? smem_desc_mn_sw128(sa, 8192u, 1024u) : smem_desc_sw128(sa);
@@ -641,10 +706,10 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                             const uint64_t bx = bd + (SPLIT ? term_q(x) * (b_bytes >> 4) : 0);
 #pragma unroll
                             for (int kk = 0; kk < kBK / 16; ++kk)
-                                umma_bf16(d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
+                                mma_if<false>(one, d_tmem, ax + astep * kk, bx + bstep * kk, idesc,
                                           (k > 0 || x > 0 || kk > 0) ? 1u : 0u);
                         }
-                        umma_commit(empty0 + 8 * stage);
+                        commit_if(one, empty0 + 8 * stage);
                     }
                     __syncwarp();
                     any = true;
@@ -653,7 +718,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                         phase ^= 1u;
                     }
                 }
-                if (ok && one) umma_commit(tfull0 + 8 * acc);
+                commit_if(ok ? one : 0u, tfull0 + 8 * acc);
                 __syncwarp();
             }
         });
@@ -736,7 +801,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
 }
 
 ProdArgs prod_args(const TcProduct &t) {
-    return ProdArgs{t.M, t.Nn, (t.K + kBK - 1) / kBK, t.p_mn ? 1 : 0, t.q_mn ? 1 : 0, t.epi};
+    return ProdArgs{t.M, t.Nn, (t.K + kBK - 1) / kBK, t.p_mn ? 1 : 0, t.q_mn ? 1 : 0, 0, t.epi};
 }
 
 // Tensor maps of both operands: `planes` planes of [k][row] or [row][k], each
@@ -747,29 +812,68 @@ bool operand_map(CUtensorMap *m, const void *base, int planes, int64_t rows, int
     return make_tmap_bf16_3d(m, base, planes, static_cast<int>(outer), static_cast<int>(inner), mn ? 64 : box);
 }
 
-int pair_units(const TcProduct &t, bool fp32) {
-    const int tm = pair_tile_m(fp32);
+int pair_units(const TcProduct &t, int tm) {
     return static_cast<int>((t.M + tm - 1) / tm) * ((t.Nn + 255) / 256);
+}
+
+// Time of one K block of a tile of tm rows, in cycles.  The MMAs of a bf16 tile
+// take 2 tm; the rest was measured (2048 x 12288 x 1280 in one round of 256, one
+// of 192, two of 128: 68, 53 and 81 us).  fp32 tiles: six products, 1.14 us at
+// 128 rows and 1.61 at 192.
+int tile_cycles(int tm, bool fp32) {
+    if (fp32) return tm == 128 ? 2170 : 3060;
+    return tm == 128 ? 303 : tm == 192 ? 399 : 512;
+}
+
+// How a launch deals its units: see PairArgs.
+struct PairPlan {
+    int tm[2], units[2];
+    int late, early;
+    int64_t cycles;
+};
+
+// The tile heights (and, with two products, the early units) that finish first.
+// At 2048 x 1280, 40 tiles of 256 rows leave half the pairs without work and 80
+// of 128 take two rounds; 55 of 192 take one.
+PairPlan pair_plan(const TcProduct *t, int count, bool fp32, int pairs) {
+    PairPlan best{};
+    best.cycles = INT64_MAX;
+    for (int tm0 = pair_max_tm(fp32); tm0 >= 128; tm0 -= 64) {
+        const int n0 = pair_units(t[0], tm0);
+        const int64_t u0 = static_cast<int64_t>((t[0].K + kBK - 1) / kBK) * tile_cycles(tm0, fp32);
+        const int late = n0 % pairs;
+        const int64_t low = n0 / pairs * u0, high = low + (late != 0 ? u0 : 0);
+        if (count == 1) {
+            if (high < best.cycles) best = PairPlan{{tm0, 0}, {n0, 0}, 0, 0, high};
+            continue;
+        }
+        for (int tm1 = pair_max_tm(fp32); tm1 >= 128; tm1 -= 64) {
+            const int n1 = pair_units(t[1], tm1);
+            const int64_t u1 = static_cast<int64_t>((t[1].K + kBK - 1) / kBK) * tile_cycles(tm1, fp32);
+            const int first = late != 0 ? static_cast<int>(u0 / u1) : 0;
+            for (int early = first; early <= first + (late != 0 ? 1 : 0); ++early) {
+                const int64_t head = static_cast<int64_t>(early) * (pairs - late);
+                int64_t end = high;
+                if (n1 <= head) {
+                    const int64_t done = low + (n1 + pairs - late - 1) / (pairs - late) * u1;
+                    if (done > end) end = done;
+                } else {
+                    if (low + early * u1 > end) end = low + early * u1;
+                    end += (n1 - head + pairs - 1) / pairs * u1;
+                }
+                if (end < best.cycles) best = PairPlan{{tm0, tm1}, {n0, n1}, late, early, end};
+            }
+        }
+    }
+    return best;
 }
 
 template <typename T, bool FULL>
 cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
-    const int planes = sizeof(T) == 4 ? 3 : 1;
-    CUtensorMap mp[2], mq[2];
-    PairArgs a{};
-    for (int i = 0; i < count; ++i) {
-        if (!operand_map(&mp[i], t[i].P, planes, t[i].Nn, t[i].K, t[i].p_mn, 128) ||
-            !operand_map(&mq[i], t[i].Q, planes, t[i].M, t[i].K, t[i].q_mn, pair_tile_m(sizeof(T) == 4) / 2))
-            return cudaErrorInvalidValue;
-        a.p[i] = prod_args(t[i]);
-        a.units[i] = pair_units(t[i], sizeof(T) == 4);
-    }
-    if (count == 1) {
-        mp[1] = mp[0];
-        mq[1] = mq[0];
-    }
-    constexpr int smem = pair_stages(sizeof(T) == 4) * pair_stage_bytes(sizeof(T) == 4) + 1024;
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr int PLANES = SPLIT ? 3 : 1;
     auto kern = linear_pair_kernel<T, FULL>;
+    constexpr int smem = kPairRing + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // pairs that fit the device at once, asked for once per device
@@ -791,13 +895,29 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
         (void)cudaGetLastError();
         if (dev < 64) fit[dev].store(pairs, std::memory_order_relaxed);
     }
-    const int total = a.units[0] + a.units[1];
-    if (pairs > total) pairs = total;
-    if (count == 2) {
-        // pairs [0, late) have one unit of the first product more than the others
-        a.late = a.units[0] % pairs;
-        a.early = a.late == 0 ? 0 : (a.p[0].kb + a.p[1].kb / 2) / a.p[1].kb;
+    CUtensorMap mp[2], mq[2];
+    PairArgs a{};
+    if (pairs > pair_units(t[0], 128) + (count == 2 ? pair_units(t[1], 128) : 0))
+        pairs = pair_units(t[0], 128) + (count == 2 ? pair_units(t[1], 128) : 0);
+    const PairPlan plan = pair_plan(t, count, SPLIT, pairs);
+    a.late = plan.late;
+    a.early = plan.early;
+    for (int i = 0; i < count; ++i) {
+        a.p[i] = prod_args(t[i]);
+        a.p[i].tm = plan.tm[i];
+        a.units[i] = plan.units[i];
+        const int q = pair_q_bytes(a.p[i].tm, t[i].q_mn);
+        if (q > a.q_room) a.q_room = q;
+        if (!operand_map(&mp[i], t[i].P, PLANES, t[i].Nn, t[i].K, t[i].p_mn, 128) ||
+            !operand_map(&mq[i], t[i].Q, PLANES, t[i].M, t[i].K, t[i].q_mn, a.p[i].tm / 2))
+            return cudaErrorInvalidValue;
     }
+    if (count == 1) {
+        mp[1] = mp[0];
+        mq[1] = mq[0];
+    }
+    a.stages = kPairRing / (PLANES * (128 * kBK * 2 + a.q_room));
+    if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     a.timeout_ns = timeout_ns;
     return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
 }
@@ -836,7 +956,10 @@ cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStr
 }
 
 // Whether a product has tiles enough to run on CTA pairs.
-bool use_pairs(const TcProduct &t, bool fp32, int num_sms) { return pair_units(t, fp32) * 2 >= num_sms / 2; }
+bool use_pairs(const TcProduct &t, bool fp32, int num_sms) {
+    const PairPlan p = pair_plan(&t, 1, fp32, num_sms / 2);
+    return p.units[0] * 2 >= num_sms / 2;
+}
 
 template <typename T>
 cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
