@@ -2,8 +2,8 @@
 // projections) and its backward pass:
 //   z = x W^T + b,  y = round(act(z) + residual),  z_out = round(z)
 //   dZ = dy act'(z),  dx = dZ W,  dW = dZ^T x,  db = sum over rows of dZ
-// This file holds the CUDA-core products, which take every type, size and
-// alignment, and the host-side choice between them and the tensor cores.
+// This file holds the passes around the products (operands for the tensor cores,
+// dZ, db) and the host-side choice between the products' kernels.
 #include "common.cuh"
 #include "internal.h"
 #include "linear.cuh"
@@ -12,71 +12,6 @@
 namespace moe {
 
 namespace {
-
-// ---------------------------------------------------------------- any size, on CUDA cores
-// C[i][j] = sum_k A(i, k) B(j, k) in fp32, 64 x 64 tiles, 4 x 4 per thread.
-// A(i, k) = A[i * ai + k * ak], and B alike, so one kernel serves the forward
-// (both rows contiguous), dx (B column-strided) and dW (both).
-struct SimtArgs {
-    const void *A, *B;
-    int64_t ai, ak, bj, bk;
-    int64_t M, Nn, K;
-    LinearEpi epi;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-linear_simt_kernel(const SimtArgs p) {
-    constexpr int BT = 64, BK = 16;
-    __shared__ float As[BK][BT + 1], Bs[BK][BT + 1];
-    pdl_trigger();
-    pdl_wait();
-    const T *A = static_cast<const T *>(p.A), *B = static_cast<const T *>(p.B);
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * BT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.y) * BT; i0 < p.M; i0 += static_cast<int64_t>(gridDim.y) * BT) {
-        float acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < p.K; k0 += BK) {
-            for (int q = threadIdx.x; q < BT * BK; q += 256) {
-                // neighbouring threads along the contiguous axis
-                const int ai = (p.ak == 1) ? q / BK : q % BT, akk = (p.ak == 1) ? q % BK : q / BT;
-                const int bj = (p.bk == 1) ? q / BK : q % BT, bkk = (p.bk == 1) ? q % BK : q / BT;
-                As[akk][ai] = (i0 + ai < p.M && k0 + akk < p.K) ? to_f32<T>(A[(i0 + ai) * p.ai + (k0 + akk) * p.ak]) : 0.0f;
-                Bs[bkk][bj] = (j0 + bj < p.Nn && k0 + bkk < p.K) ? to_f32<T>(B[(j0 + bj) * p.bj + (k0 + bkk) * p.bk]) : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < BK; ++k) {
-                float a[4], b[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    a[u] = As[k][ty + 16 * u];
-                    b[u] = Bs[k][tx + 16 * u];
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[u], b[v], acc[u][v]);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-                if (i < p.M && j < p.Nn) linear_store<T>(p.epi, i, j, p.Nn, acc[u][v]);
-            }
-    }
-}
-
-template <typename T>
-cudaError_t launch_simt(const SimtArgs &p, cudaStream_t s) {
-    const int64_t gy = (p.M + 63) / 64;
-    return launch_pdl(linear_simt_kernel<T>,
-                      dim3(static_cast<unsigned>((p.Nn + 63) / 64), static_cast<unsigned>(gy < 32768 ? gy : 32768)),
-                      dim3(256), 0, s, p);
-}
 
 // ---------------------------------------------------------------- operands for the tensor cores
 // v = p0 + p1 + p2 in bf16 parts (each the rest rounded to bf16; the rests are
@@ -129,24 +64,28 @@ __device__ __forceinline__ void put_operand8(__nv_bfloat16 *out, int64_t at, int
     for (int k = 0; k < PARTS; ++k) *reinterpret_cast<uint4 *>(out + at + k * plane) = raw[k];
 }
 
-// An array as an operand: rows padded with zeros to ld (a multiple of 8), fp32
-// values in parts.  One thread per eight elements; I: index type that holds them all.
+// One or two arrays of the same width as operands: rows padded with zeros to ld
+// (a multiple of 8), fp32 values in parts.  One thread per eight elements; I:
+// index type that holds them all.
 template <typename T, typename I>
 __global__ void __launch_bounds__(256)
-linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __nv_bfloat16 *out) {
+linear_pack_kernel(const T *__restrict__ in0, int64_t rows0, __nv_bfloat16 *out0, const T *__restrict__ in1,
+                   int64_t rows1, __nv_bfloat16 *out1, int cols, int ld) {
     pdl_trigger();
     pdl_wait();
     const bool vec = cols % 8 == 0;
-    const I per_row = static_cast<I>(ld / 8), total = static_cast<I>(rows) * per_row;
+    const I per_row = static_cast<I>(ld / 8), total = static_cast<I>(rows0 + rows1) * per_row;
     for (I i = static_cast<I>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<I>(gridDim.x) * 256) {
         const I r = i / per_row;
         const int c = static_cast<int>(i - r * per_row) * 8;
-        Eight<T> in8;
-        in8.load(in + static_cast<int64_t>(r) * cols, c, cols, vec);
+        const bool second = static_cast<int64_t>(r) >= rows0;
+        const int64_t row = static_cast<int64_t>(r) - (second ? rows0 : 0), rows = second ? rows1 : rows0;
+        Eight<T> e;
+        e.load((second ? in1 : in0) + row * cols, c, cols, vec);
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = in8[k];
-        put_operand8<T>(out, static_cast<int64_t>(i) * 8, rows * ld, v);
+        for (int k = 0; k < 8; ++k) v[k] = e[k];
+        put_operand8<T>(second ? out1 : out0, row * ld + c, rows * ld, v);
     }
 }
 
@@ -154,8 +93,8 @@ linear_pack_kernel(const T *__restrict__ in, int64_t rows, int cols, int ld, __n
 // dZ = dy act'(z), rounded to the storage type and laid out as an operand, and
 // the column sums of the unrounded dZ over a chunk of rows.  A block takes 256
 // columns, eight to a lane, its 8 warps every eighth row of the chunk, ROWS at a
-// time.  dz and part nullable.  O: bf16 for an operand (fp32 in parts), T for
-// the CUDA-core products.
+// time.  dz and part nullable.  O: bf16 for an operand (fp32 in parts), or T
+// with ld = n for the CUDA-core products.
 template <typename T, typename O>
 __global__ void __launch_bounds__(256, 2)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
@@ -265,31 +204,51 @@ size_t operand_bytes(int64_t rows, int cols, int dt) {
     return align_up(static_cast<size_t>(rows) * pad8(cols) * 2 * (dt == 0 ? 3 : 1), 256);
 }
 
-// `in` as an operand at `out` (scratch) if it is not one already.
+// Arrays of the same width as operands in scratch, in one launch; in1 nullable.
 template <typename T>
-cudaError_t pack(const void *&in, int64_t rows, int cols, void *out, cudaStream_t s) {
-    if (!needs_pack(sizeof(T) == 2 ? 1 : 0, cols)) return cudaSuccess;
-    const int64_t n = rows * (pad8(cols) / 8), blocks = (n + 255) / 256;
+cudaError_t pack(const void *&in0, int64_t rows0, void *out0, const void *&in1, int64_t rows1, void *out1, int cols,
+                 cudaStream_t s) {
+    const int64_t n = (rows0 + rows1) * (pad8(cols) / 8), blocks = (n + 255) / 256;
     const bool small = n + 256 * 2368 < UINT32_MAX;
     cudaError_t e = launch_pdl(small ? linear_pack_kernel<T, uint32_t> : linear_pack_kernel<T, int64_t>,
                                dim3(static_cast<unsigned>(blocks < 2368 ? blocks : 2368)), dim3(256), 0, s,
-                               static_cast<const T *>(in), rows, cols, pad8(cols), static_cast<__nv_bfloat16 *>(out));
-    in = out;
+                               static_cast<const T *>(in0), rows0, static_cast<__nv_bfloat16 *>(out0),
+                               static_cast<const T *>(in1), rows1, static_cast<__nv_bfloat16 *>(out1), cols, pad8(cols));
+    if (rows0 > 0) in0 = out0;
+    if (rows1 > 0) in1 = out1;
     return e;
 }
 
-// Products too small for the tensor-core kernels' setup run on CUDA cores.
-bool use_simt(int64_t M, int d_in, int d_out) { return M * d_in * static_cast<int64_t>(d_out) <= (1 << 18); }
+// A few tokens: the CUDA-core kernels, unless W is already an operand, which
+// streams as fast through the tensor cores (dW has no such form).
+bool use_skinny(int64_t M, int dt, int cols) { return M <= kSkinnyRows && needs_pack(dt, cols); }
+bool use_skinny_dw(int64_t M) { return M <= kSkinnyRows; }
 
 struct FwdScratch {
     size_t x, W, total;
 };
 FwdScratch fwd_scratch(int64_t M, int d_in, int d_out, int dt) {
     FwdScratch L{};
-    if (M == 0 || use_simt(M, d_in, d_out) || !needs_pack(dt, d_in)) return L;
+    if (M == 0 || !needs_pack(dt, d_in) || use_skinny(M, dt, d_in)) return L;
     L.W = operand_bytes(M, d_in, dt);
     L.total = L.W + operand_bytes(d_out, d_in, dt);
     return L;
+}
+
+// What a backward call's products read: dZ as rows of the storage type for the
+// CUDA-core kernels, as an operand for the tensor cores (never both).
+struct BwdWays {
+    bool dx_skinny, dw_skinny;
+    bool dz_rows, dz_operand;  // dZ is written to scratch in this form
+};
+BwdWays bwd_ways(int64_t M, int d_in, int d_out, int dt, int act) {
+    BwdWays w{};
+    w.dw_skinny = use_skinny_dw(M);
+    w.dx_skinny = w.dw_skinny && (use_skinny(M, dt, d_in) || needs_pack(dt, d_out));
+    // rows are an operand already when bf16 and a multiple of 8 wide
+    w.dz_rows = w.dw_skinny && act != kActNone;
+    w.dz_operand = !w.dw_skinny && (act != kActNone || needs_pack(dt, d_out));
+    return w;
 }
 
 // Byte offsets inside the backward workspace: dZ, x and W as operands, and the
@@ -298,19 +257,16 @@ struct BwdScratch {
     size_t dz, x, W, part, total;
 };
 BwdScratch bwd_scratch(int64_t M, int d_in, int d_out, int dt, int act) {
+    const BwdWays w = bwd_ways(M, d_in, d_out, dt, act);
     BwdScratch L{};
     size_t o = 0;
-    const bool simt = use_simt(M, d_in, d_out);
     L.dz = o;
-    if (simt) {
-        if (act != kActNone) o += align_up(static_cast<size_t>(M) * d_out * 4, 256);
-    } else if (act != kActNone || needs_pack(dt, d_out)) {
-        o += operand_bytes(M, d_out, dt);
-    }
+    if (w.dz_rows) o += align_up(static_cast<size_t>(M) * d_out * (dt == 1 ? 2 : 4), 256);
+    if (w.dz_operand) o += operand_bytes(M, d_out, dt);
     L.x = o;
-    if (!simt && needs_pack(dt, d_in)) o += operand_bytes(M, d_in, dt);
+    if (!w.dw_skinny && needs_pack(dt, d_in)) o += operand_bytes(M, d_in, dt);
     L.W = o;
-    if (!simt && needs_pack(dt, d_in)) o += operand_bytes(d_out, d_in, dt);
+    if (!w.dx_skinny && needs_pack(dt, d_in)) o += operand_bytes(d_out, d_in, dt);
     L.part = o;
     o += align_up(static_cast<size_t>(row_chunks(M, d_out)) * d_out * sizeof(float), 256);
     L.total = o;
@@ -326,16 +282,16 @@ cudaError_t launch_linear(const LinearArgs &a, void *ws, uint64_t timeout_ns, in
     const LinearEpi epi{a.b, a.act, a.residual, a.y, a.z_out};
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        if (use_simt(a.M, a.d_in, a.d_out)) {
-            SimtArgs p{a.x, a.W, a.d_in, 1, a.d_in, 1, a.M, a.d_out, a.d_in, epi};
-            return launch_simt<T>(p, s);
-        }
-        const FwdScratch L = fwd_scratch(a.M, a.d_in, a.d_out, a.dt);
-        uint8_t *w = static_cast<uint8_t *>(ws);
+        if (use_skinny(a.M, a.dt, a.d_in))
+            return launch_skinny_fwd<T>(static_cast<const T *>(a.x), static_cast<const T *>(a.W), a.M, a.d_in, a.d_out,
+                                        epi, s);
         const void *x = a.x, *W = a.W;
-        cudaError_t e = pack<T>(x, a.M, a.d_in, w + L.x, s);
-        if (e == cudaSuccess) e = pack<T>(W, a.d_out, a.d_in, w + L.W, s);
-        if (e != cudaSuccess) return e;
+        if (needs_pack(a.dt, a.d_in)) {
+            const FwdScratch L = fwd_scratch(a.M, a.d_in, a.d_out, a.dt);
+            uint8_t *w = static_cast<uint8_t *>(ws);
+            cudaError_t e = pack<T>(x, a.M, w + L.x, W, a.d_out, w + L.W, a.d_in, s);
+            if (e != cudaSuccess) return e;
+        }
         const TcProduct t{W, x, a.M, a.d_out, a.d_in, false, false, epi};
         return launch_tc_products(&t, 1, sizeof(T) == 4, true, timeout_ns, num_sms, s);
     };
@@ -354,59 +310,61 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         if (e == cudaSuccess && a.db != nullptr) e = cudaMemsetAsync(a.db, 0, sizeof(float) * static_cast<size_t>(a.d_out), s);
         return e;
     }
+    const BwdWays ways = bwd_ways(a.M, a.d_in, a.d_out, a.dt, a.act);
     const BwdScratch L = bwd_scratch(a.M, a.d_in, a.d_out, a.dt, a.act);
     uint8_t *w = static_cast<uint8_t *>(ws);
     auto go = [&](auto tag) {
         using T = decltype(tag);
         cudaError_t e = cudaSuccess;
-        const bool simt = use_simt(a.M, a.d_in, a.d_out);
         const bool products = a.dx != nullptr || a.dW != nullptr;
-        const bool make_dz = products && (a.act != kActNone || (!simt && needs_pack(a.dt, a.d_out)));
+        const bool rows = products && ways.dz_rows, operand = products && ways.dz_operand;
         float *part = a.db != nullptr ? reinterpret_cast<float *>(w + L.part) : nullptr;
         const int64_t chunks = row_chunks(a.M, a.d_out);
-        const void *dz = make_dz ? static_cast<const void *>(w + L.dz) : a.dy;
-        if (make_dz || part != nullptr) {
-            // on CUDA cores dZ stays in the storage type; otherwise it is laid out as an operand
-            const int ld = simt ? a.d_out : pad8(a.d_out);
+        const void *dz = rows || operand ? static_cast<const void *>(w + L.dz) : a.dy;
+        if (rows || operand || part != nullptr) {
+            const int ld = operand ? pad8(a.d_out) : a.d_out;
             const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(ld) + 255) / 256), static_cast<unsigned>(chunks));
-            if (simt)
-                e = launch_pdl(linear_dz_kernel<T, T>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
-                               static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
-                               make_dz ? reinterpret_cast<T *>(w + L.dz) : nullptr, part);
-            else
-                e = launch_pdl(linear_dz_kernel<T, __nv_bfloat16>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
-                               static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
-                               make_dz ? reinterpret_cast<__nv_bfloat16 *>(w + L.dz) : nullptr, part);
+            auto dz_pass = [&](auto out) {
+                using O = decltype(out);
+                return launch_pdl(linear_dz_kernel<T, O>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
+                                  static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
+                                  rows || operand ? reinterpret_cast<O *>(w + L.dz) : static_cast<O *>(nullptr),
+                                  chunks == 1 ? a.db : part);
+            };
+            e = rows ? dz_pass(T{}) : dz_pass(__nv_bfloat16{});
             if (e != cudaSuccess) return e;
         }
-        if (part != nullptr) {
+        if (part != nullptr && chunks > 1) {
             e = launch_pdl(linear_db_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(a.d_out) + 31) / 32)),
                            dim3(1024), 0, s, part, chunks, a.d_out, a.db);
             if (e != cudaSuccess) return e;
         }
         if (!products) return e;
-        if (simt) {
-            if (a.dx != nullptr) {
-                SimtArgs p{dz, a.W, a.d_out, 1, 1, a.d_in, a.M, a.d_in, a.d_out, {nullptr, kActNone, nullptr, a.dx, nullptr}};
-                if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
-            }
-            if (a.dW != nullptr) {
-                SimtArgs p{dz, a.x, 1, a.d_out, 1, a.d_in, a.d_out, a.d_in, a.M, {nullptr, kActNone, nullptr, a.dW, nullptr}};
-                if ((e = launch_simt<T>(p, s)) != cudaSuccess) return e;
-            }
-            return e;
-        }
+        const bool tc_dw = a.dW != nullptr && !ways.dw_skinny, tc_dx = a.dx != nullptr && !ways.dx_skinny;
         const void *x = a.x, *W = a.W;
-        if (a.dW != nullptr) e = pack<T>(x, a.M, a.d_in, w + L.x, s);
-        if (e == cudaSuccess && a.dx != nullptr) e = pack<T>(W, a.d_out, a.d_in, w + L.W, s);
-        if (e != cudaSuccess) return e;
+        if (needs_pack(a.dt, a.d_in) && (tc_dw || tc_dx)) {
+            e = pack<T>(x, tc_dw ? a.M : 0, w + L.x, W, tc_dx ? a.d_out : 0, w + L.W, a.d_in, s);
+            if (e != cudaSuccess) return e;
+        }
         TcProduct t[2];
         int n = 0;
-        if (a.dW != nullptr)
+        if (tc_dw)
             t[n++] = TcProduct{x, dz, a.d_out, a.d_in, static_cast<int>(a.M), true, true, {nullptr, kActNone, nullptr, a.dW, nullptr}};
-        if (a.dx != nullptr)
+        if (tc_dx)
             t[n++] = TcProduct{W, dz, a.M, a.d_in, a.d_out, true, false, {nullptr, kActNone, nullptr, a.dx, nullptr}};
-        return launch_tc_products(t, n, sizeof(T) == 4, false, timeout_ns, num_sms, s);
+        if (n > 0) {
+            e = launch_tc_products(t, n, sizeof(T) == 4, false, timeout_ns, num_sms, s);
+            if (e != cudaSuccess) return e;
+        }
+        if (a.dx != nullptr && ways.dx_skinny) {
+            e = launch_skinny_dx<T>(static_cast<const T *>(dz), static_cast<const T *>(a.W), a.M, a.d_in, a.d_out,
+                                    static_cast<T *>(a.dx), s);
+            if (e != cudaSuccess) return e;
+        }
+        if (a.dW != nullptr && ways.dw_skinny)
+            e = launch_skinny_dw<T>(static_cast<const T *>(dz), static_cast<const T *>(a.x), a.M, a.d_in, a.d_out,
+                                    static_cast<T *>(a.dW), s);
+        return e;
     };
     return a.dt == 1 ? go(__nv_bfloat16{}) : go(float{});
 }

@@ -1,0 +1,299 @@
+// The dense layer's products for a few tokens (M <= 16), on CUDA cores: each
+// weight is read once (or written once, for dW) with 16-byte accesses and meets
+// all M tokens in registers, so the kernels run at the rate of W's bytes and
+// need no copy of W in another form.  fp32 accumulation in fp32 storage too.
+//   forward  z[m][n]  = sum_k x[m][k] W[n][k]       rows of W, K split over a block's warps
+//   dx       dx[m][i] = sum_o dZ[m][o] W[o][i]      columns of W, o split over warps and a cluster
+//   dW       dW[o][i] = sum_m dZ[m][o] x[m][i]      one pass over dW
+// The multiply-adds stay below the bytes' time: a warp's 512 bytes of W take
+// 4 M of them, 16 cycles an SM at M = 16, against 22 cycles at HBM's rate.
+// VEC: elements of a 16-byte vector, or 1 where rows do not start on 16 bytes.
+#include "common.cuh"
+#include "internal.h"
+#include "linear.cuh"
+#include "linear_tc.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = to_f32<T>(*p);
+    } else {
+        const uint4 raw = *reinterpret_cast<const uint4 *>(p);
+        const T *e = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f32<T>(e[i]);
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        *p = from_f32<T>(v[0]);
+    } else {
+        uint4 raw;
+        T *e = reinterpret_cast<T *>(&raw);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) e[i] = from_f32<T>(v[i]);
+        *reinterpret_cast<uint4 *>(p) = raw;
+    }
+}
+
+// ---------------------------------------------------------------- forward
+// A block takes R rows of W; warp w the vectors w, w + 8, ... of K.
+template <typename T, int VEC, int MT, int R>
+__global__ void __launch_bounds__(kThreads)
+skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K, int Nn, const LinearEpi epi) {
+    __shared__ float red[kWarps][R * MT];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.x * R;
+    float acc[R][MT] = {};
+    for (int k = (warp * 32 + lane) * VEC; k < K; k += kThreads * VEC) {
+        float w[R][VEC];
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_vec<T, VEC>(W + static_cast<int64_t>(n0 + r < Nn ? n0 + r : n0) * K + k, w[r]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (m < M) {
+                float a[VEC];
+                load_vec<T, VEC>(x + static_cast<int64_t>(m) * K + k, a);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) acc[r][m] = fmaf(a[i], w[r][i], acc[r][m]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float v = acc[r][m];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) red[warp][m * R + r] = v;
+        }
+    __syncthreads();
+    if (threadIdx.x < R * MT) {
+        const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+        if (m < M && n < Nn) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += red[w][threadIdx.x];
+            linear_store<T>(epi, m, n, Nn, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dx
+// A cluster of S blocks takes 32 VEC columns; block r the rows o = r, r + S, ...
+// in chunks that its 8 warps share.
+template <typename T, int VEC, int MT>
+__global__ void __launch_bounds__(kThreads)
+skinny_dx_kernel(const T *__restrict__ dz, const T *__restrict__ W, int M, int Ni, int No, int S, T *dx) {
+    constexpr int COLS = 32 * VEC, CHUNK = 64;  // rows of W a chunk: 8 a warp
+    extern __shared__ float smem[];             // [kWarps][MT][COLS]
+    __shared__ float g[CHUNK][MT];              // dZ of the chunk
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int i0 = blockIdx.x / S * COLS, col = i0 + lane * VEC;
+    float acc[MT][VEC] = {};
+    for (int base = rank * CHUNK; base < No; base += S * CHUNK) {
+        __syncthreads();
+        for (int q = threadIdx.x; q < CHUNK * MT; q += kThreads) {
+            const int m = q / CHUNK, o = q % CHUNK;
+            g[o][m] = (m < M && base + o < No) ? to_f32<T>(dz[static_cast<int64_t>(m) * No + base + o]) : 0.0f;
+        }
+        __syncthreads();
+        if (col < Ni) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float w[4][VEC];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int o = base + warp + 8 * (4 * h + u);
+                    load_vec<T, VEC>(W + static_cast<int64_t>(o < No ? o : base) * Ni + col, w[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int o = warp + 8 * (4 * h + u);
+                    if (base + o < No) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) acc[m][i] = fmaf(g[o][m], w[u][i], acc[m][i]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) smem[(warp * MT + m) * COLS + i * 32 + lane] = acc[m][i];
+    __syncthreads();
+    // the block's sums in smem[0 .. MT COLS), then the cluster's parts in rank order
+    for (int q = threadIdx.x; q < MT * COLS; q += kThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += smem[w * MT * COLS + q];
+        smem[q] = v;
+    }
+    __syncthreads();
+    if (S > 1) cluster_sync();
+    for (int q = rank * kThreads + threadIdx.x; q < M * COLS; q += S * kThreads) {
+        float v = 0.0f;
+        if (S > 1) {
+            float u[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                u[c] = 0.0f;
+                if (c < S)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u[c])
+                                 : "r"(map_to_cta(smem_u32(smem + q), c))
+                                 : "memory");
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v += u[c];
+        } else {
+            v = smem[q];
+        }
+        const int m = q / COLS, i = i0 + (q % 32) * VEC + (q % COLS) / 32;
+        if (i < Ni) dx[static_cast<int64_t>(m) * Ni + i] = from_f32<T>(v);
+    }
+    if (S > 1) cluster_sync();  // no block leaves while another reads its sums
+}
+
+// ---------------------------------------------------------------- dW
+// A block takes 32 VEC columns and 64 rows of dW: x of the columns in registers,
+// dZ of the rows in shared memory, each warp every eighth row.
+template <typename T, int VEC, int MT>
+__global__ void __launch_bounds__(kThreads)
+skinny_dw_kernel(const T *__restrict__ dz, const T *__restrict__ x, int M, int Ni, int No, T *dW) {
+    constexpr int ROWS = 64;
+    __shared__ float g[ROWS][MT];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = (blockIdx.x * 32 + lane) * VEC;
+    float a[MT][VEC];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) a[m][i] = 0.0f;
+        if (m < M && col < Ni) load_vec<T, VEC>(x + static_cast<int64_t>(m) * Ni + col, a[m]);
+    }
+    for (int64_t o0 = static_cast<int64_t>(blockIdx.y) * ROWS; o0 < No; o0 += static_cast<int64_t>(gridDim.y) * ROWS) {
+        __syncthreads();
+        for (int q = threadIdx.x; q < ROWS * MT; q += kThreads) {
+            const int m = q / ROWS, o = q % ROWS;
+            g[o][m] = (m < M && o0 + o < No) ? to_f32<T>(dz[static_cast<int64_t>(m) * No + o0 + o]) : 0.0f;
+        }
+        __syncthreads();
+        if (col < Ni) {
+#pragma unroll 2
+            for (int o = warp; o < ROWS; o += kWarps) {
+                if (o0 + o >= No) break;
+                float v[VEC] = {};
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[i] = fmaf(g[o][m], a[m][i], v[i]);
+                store_vec<T, VEC>(dW + (o0 + o) * Ni + col, v);
+            }
+        }
+    }
+}
+
+template <int V> struct Int {
+    static constexpr int value = V;
+};
+
+// f(tag of VEC, tag of MT) for rows of `cols` elements.
+template <typename T, typename F> cudaError_t skinny_pick(int cols, int64_t M, F f) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    auto with = [&](auto vec) {
+        if (M <= 1) return f(vec, Int<1>{});
+        if (M <= 4) return f(vec, Int<4>{});
+        return f(vec, Int<kSkinnyRows>{});
+    };
+    return cols % VEC == 0 ? with(Int<VEC>{}) : with(Int<1>{});
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, const LinearEpi &epi, cudaStream_t s) {
+    return skinny_pick<T>(K, M, [&](auto vec, auto mt) {
+        // rows a block: few enough that every SM has blocks, many enough to share x
+        constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
+        auto go = [&](auto r) {
+            constexpr int R = decltype(r)::value;
+            return launch_pdl(skinny_fwd_kernel<T, V, MT, R>, dim3(static_cast<unsigned>((Nn + R - 1) / R)),
+                              dim3(kThreads), 0, s, x, W, static_cast<int>(M), K, Nn, epi);
+        };
+        return Nn >= 4 * 148 * 4 ? go(Int<(MT > 4 ? 8 : 4)>{}) : go(Int<2>{});
+    });
+}
+
+template <typename T>
+cudaError_t launch_skinny_dx(const T *dz, const T *W, int64_t M, int Ni, int No, T *dx, cudaStream_t s) {
+    return skinny_pick<T>(Ni, M, [&](auto vec, auto mt) {
+        constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
+        constexpr int smem = kWarps * MT * 32 * V * static_cast<int>(sizeof(float));
+        auto kern = skinny_dx_kernel<T, V, MT>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        const int tiles = (Ni + 32 * V - 1) / (32 * V);
+        int S = (No + 63) / 64;  // a chunk of rows each at least
+        if (S > 8) S = 8;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = S;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = S > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kern, dz, W, static_cast<int>(M), Ni, No, S, dx);
+    });
+}
+
+template <typename T>
+cudaError_t launch_skinny_dw(const T *dz, const T *x, int64_t M, int Ni, int No, T *dW, cudaStream_t s) {
+    return skinny_pick<T>(Ni, M, [&](auto vec, auto mt) {
+        constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
+        const int64_t gy = (static_cast<int64_t>(No) + 63) / 64;
+        return launch_pdl(skinny_dw_kernel<T, V, MT>,
+                          dim3(static_cast<unsigned>((Ni + 32 * V - 1) / (32 * V)), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
+                          dim3(kThreads), 0, s, dz, x, static_cast<int>(M), Ni, No, dW);
+    });
+}
+
+template cudaError_t launch_skinny_fwd<float>(const float *, const float *, int64_t, int, int, const LinearEpi &, cudaStream_t);
+template cudaError_t launch_skinny_fwd<__nv_bfloat16>(const __nv_bfloat16 *, const __nv_bfloat16 *, int64_t, int, int,
+                                                      const LinearEpi &, cudaStream_t);
+template cudaError_t launch_skinny_dx<float>(const float *, const float *, int64_t, int, int, float *, cudaStream_t);
+template cudaError_t launch_skinny_dx<__nv_bfloat16>(const __nv_bfloat16 *, const __nv_bfloat16 *, int64_t, int, int,
+                                                     __nv_bfloat16 *, cudaStream_t);
+template cudaError_t launch_skinny_dw<float>(const float *, const float *, int64_t, int, int, float *, cudaStream_t);
+template cudaError_t launch_skinny_dw<__nv_bfloat16>(const __nv_bfloat16 *, const __nv_bfloat16 *, int64_t, int, int,
+                                                     __nv_bfloat16 *, cudaStream_t);
+
+}  // namespace moe

@@ -556,6 +556,39 @@ constexpr int kSplitSmem = 216 * 1024;
 
 template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
 
+// Adds the cluster's S <= C parts of columns [j0, j0 + mine) of this lane's n, in
+// rank order, and stores them: 32 loads in flight (loaded one after the other
+// they took 10 us of a 28 us decode product).
+template <typename T, int C>
+__device__ __forceinline__ void add_parts(const ProdArgs &p, uint32_t at, int S, int j0, int mine, int64_t m0, int n,
+                                          float bias) {
+    constexpr int J = 32 / C;
+    uint32_t peer[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) peer[c] = map_to_cta(at, c < S ? c : 0);
+    for (int j = 0; j < mine; j += J) {
+        float u[J][C], v[J];
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                u[i][c] = 0.0f;
+                if (c < S && j + i < mine)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u[i][c])
+                                 : "r"(peer[c] + static_cast<uint32_t>(j0 + j + i) * 512u)
+                                 : "memory");
+            }
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+            v[i] = u[i][0];
+#pragma unroll
+            for (int c = 1; c < C; ++c) v[i] += u[i][c];
+        }
+        store_cols<T, true, J>(p.epi, v, m0 + j0 + j, n, p.Nn, mine - j, bias);
+    }
+}
+
 template <typename T, int BN>
 __global__ void __launch_bounds__(kSplitThreads, split_ctas(sizeof(T) == 4))
 linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constant__ CUtensorMap tq, const ProdArgs p,
@@ -766,23 +799,11 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
         cluster_sync();
         if (warp >= 2 && n < p.Nn) {
             const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
-            for (int j = rank; j < rows; j += S) {
-                float v = 0.0f;
-                for (int c = 0; c < S; ++c) {
-                    float u;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(u)
-                                 : "r"(map_to_cta(smem_base + static_cast<uint32_t>(j * 128 + lane_n) * 4u, c))
-                                 : "memory");
-                    v += u;
-                }
-                const int64_t at = (m0 + j) * p.Nn + n;
-                v += bias;
-                if (p.epi.z_out != nullptr) static_cast<T *>(p.epi.z_out)[at] = from_f32<T>(v);
-                v = act_value(v, p.epi.act);
-                if (p.epi.residual != nullptr) v += to_f32<T>(static_cast<const T *>(p.epi.residual)[at]);
-                static_cast<T *>(p.epi.out)[at] = from_f32<T>(v);
-            }
+            const int share = (rows + S - 1) / S, j0 = rank * share;
+            const int mine = rows - j0 < share ? rows - j0 : share;
+            if (S <= 2) add_parts<T, 2>(p, smem_base + static_cast<uint32_t>(lane_n) * 4u, S, j0, mine, m0, n, bias);
+            else if (S <= 4) add_parts<T, 4>(p, smem_base + static_cast<uint32_t>(lane_n) * 4u, S, j0, mine, m0, n, bias);
+            else add_parts<T, 8>(p, smem_base + static_cast<uint32_t>(lane_n) * 4u, S, j0, mine, m0, n, bias);
         }
     } else if (warp >= 2 && good && n < p.Nn) {
         const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
@@ -968,7 +989,7 @@ cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cuda
     const int kb = (t.K + kBK - 1) / kBK;
     int S = static_cast<int>(split_ctas(sizeof(T) == 4) * num_sms / tiles);
     if (S > 8) S = 8;
-    if (S > kb) S = kb;
+    if (S > kb / 2) S = kb / 2;  // two K blocks a CTA at least
     if (S < 1) S = 1;
     switch (bn) {
     case 16: return launch_split<T, 16>(t, S, timeout_ns, s);

@@ -1,4 +1,5 @@
-// Tensor-core products of the dense layer (linear_tc.cu), used by linear.cu.
+// Products of the dense layer, used by linear.cu: on the tensor cores
+// (linear_tc.cu) and, for a few tokens, on CUDA cores (linear_skinny.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -24,5 +25,14 @@ struct TcProduct {
 // full: bias, activation, residual and z of the epilogue; else out alone.
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s);
+
+// M <= kSkinnyRows tokens; rows dense, of any width.  dz: dZ in the storage type.
+constexpr int kSkinnyRows = 16;
+template <typename T>
+cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, const LinearEpi &epi, cudaStream_t s);
+template <typename T>
+cudaError_t launch_skinny_dx(const T *dz, const T *W, int64_t M, int Ni, int No, T *dx, cudaStream_t s);
+template <typename T>
+cudaError_t launch_skinny_dw(const T *dz, const T *x, int64_t M, int Ni, int No, T *dW, cudaStream_t s);
 
 }  // namespace moe
