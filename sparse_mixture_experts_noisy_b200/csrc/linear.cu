@@ -348,9 +348,9 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         }
         TcProduct t[2];
         int n = 0;
-        if (tc_dw)
+        if (!ways.dw_skinny)
             t[n++] = TcProduct{x, dz, a.d_out, a.d_in, static_cast<int>(a.M), true, true, {nullptr, kActNone, nullptr, a.dW, nullptr}};
-        if (tc_dx)
+        if (!ways.dx_skinny)
             t[n++] = TcProduct{W, dz, a.M, a.d_in, a.d_out, true, false, {nullptr, kActNone, nullptr, a.dx, nullptr}};
         if (n > 0) {
             e = launch_tc_products(t, n, sizeof(T) == 4, false, timeout_ns, num_sms, s);

@@ -45,49 +45,77 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
 }
 
 // ---------------------------------------------------------------- forward
-// A block takes R rows of W; warp w the vectors w, w + 8, ... of K.
-template <typename T, int VEC, int MT, int R>
+// Sums V values of each lane over the warp (V a multiple of 32, or at most 32 and
+// a power of two): each step halves the values a lane still carries.  After it
+// lane l holds the totals of values l V / 32 + i in v[i] (V >= 32), or of value
+// l / (32 / V) in v[0].
+template <int V>
+__device__ __forceinline__ void fold(float *v, int lane) {
+    int n = V;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            n /= 2;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                if (i < n) {
+                    const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+}
+
+// A warp group of KW warps takes R rows of W; its warp w the vectors w, w + KW,
+// ... of K.
+template <typename T, int VEC, int MT, int R, int KW>
 __global__ void __launch_bounds__(kThreads)
 skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K, int Nn, const LinearEpi epi) {
-    __shared__ float red[kWarps][R * MT];
+    constexpr int V = R * MT, GROUPS = kWarps / KW;
+    static_assert(V % 32 == 0 || (V < 32 && (V & (V - 1)) == 0), "fold");
+    __shared__ float red[kWarps][V];
     pdl_trigger();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * R;
-    float acc[R][MT] = {};
-    for (int k = (warp * 32 + lane) * VEC; k < K; k += kThreads * VEC) {
-        float w[R][VEC];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = warp / KW;
+    const int n0 = (blockIdx.x * GROUPS + grp) * R;
+    float acc[V] = {};  // [r][m]
+    if (n0 < Nn) {
+        for (int k = (warp % KW * 32 + lane) * VEC; k < K; k += KW * 32 * VEC) {
+            float w[R][VEC];
 #pragma unroll
-        for (int r = 0; r < R; ++r) load_vec<T, VEC>(W + static_cast<int64_t>(n0 + r < Nn ? n0 + r : n0) * K + k, w[r]);
+            for (int r = 0; r < R; ++r)
+                load_vec<T, VEC>(W + static_cast<int64_t>(n0 + r < Nn ? n0 + r : n0) * K + k, w[r]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (m < M) {
-                float a[VEC];
-                load_vec<T, VEC>(x + static_cast<int64_t>(m) * K + k, a);
+            for (int m = 0; m < MT; ++m) {
+                if (m < M) {
+                    float a[VEC];
+                    load_vec<T, VEC>(x + static_cast<int64_t>(m) * K + k, a);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[r][m] = fmaf(a[i], w[r][i], acc[r][m]);
+                        for (int i = 0; i < VEC; ++i) acc[r * MT + m] = fmaf(a[i], w[r][i], acc[r * MT + m]);
+                }
             }
         }
     }
+    fold<V>(acc, lane);
+    if constexpr (V >= 32) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float v = acc[r][m];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) red[warp][m * R + r] = v;
-        }
+        for (int i = 0; i < V / 32; ++i) red[warp][lane * (V / 32) + i] = acc[i];
+    } else {
+        if (lane % (32 / V) == 0) red[warp][lane / (32 / V)] = acc[0];
+    }
     __syncthreads();
-    if (threadIdx.x < R * MT) {
-        const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+    for (int q = threadIdx.x; q < GROUPS * V; q += kThreads) {
+        const int g = q / V, v = q % V, m = v % MT, n = (blockIdx.x * GROUPS + g) * R + v / MT;
         if (m < M && n < Nn) {
-            float v = 0.0f;
+            float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += red[w][threadIdx.x];
-            linear_store<T>(epi, m, n, Nn, v);
+            for (int w = 0; w < KW; ++w) sum += red[g * KW + w][v];
+            linear_store<T>(epi, m, n, Nn, sum);
         }
     }
 }
@@ -235,14 +263,16 @@ template <typename T, typename F> cudaError_t skinny_pick(int cols, int64_t M, F
 template <typename T>
 cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, const LinearEpi &epi, cudaStream_t s) {
     return skinny_pick<T>(K, M, [&](auto vec, auto mt) {
-        // rows a block: few enough that every SM has blocks, many enough to share x
+        // rows a warp group: enough to share x, few enough that the SMs have blocks.  A
+        // group is a warp where a row gives it work for four vectors a lane.
         constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
-        auto go = [&](auto r) {
-            constexpr int R = decltype(r)::value;
-            return launch_pdl(skinny_fwd_kernel<T, V, MT, R>, dim3(static_cast<unsigned>((Nn + R - 1) / R)),
+        auto go = [&](auto r, auto kw) {
+            constexpr int R = decltype(r)::value, KW = decltype(kw)::value, rows = R * (kWarps / KW);
+            return launch_pdl(skinny_fwd_kernel<T, V, MT, R, KW>, dim3(static_cast<unsigned>((Nn + rows - 1) / rows)),
                               dim3(kThreads), 0, s, x, W, static_cast<int>(M), K, Nn, epi);
         };
-        return Nn >= 4 * 148 * 4 ? go(Int<(MT > 4 ? 8 : 4)>{}) : go(Int<2>{});
+        constexpr int R = MT > 1 ? 4 : 2;
+        return K >= 8 * 32 * V || Nn < 148 * kWarps ? go(Int<R>{}, Int<kWarps>{}) : go(Int<R>{}, Int<1>{});
     });
 }
 

@@ -186,21 +186,22 @@ __device__ __forceinline__ void put_cols(T *p, const float (&v)[CN], int ld, int
     }
 }
 
+// The residual's values at CN columns (a valid one in place of those past `cols`).
+template <typename T, int CN>
+__device__ __forceinline__ void get_residual(T (&res)[CN], const LinearEpi &e, int64_t m0, int n, int ld, int cols) {
+    const T *p = static_cast<const T *>(e.residual) + m0 * ld + n;
+#pragma unroll
+    for (int i = 0; i < CN; ++i) res[i] = p[static_cast<int64_t>(i < cols ? i : 0) * ld];
+}
+
 template <typename T, bool FULL, int CN>
-__device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc, int64_t m0, int n, int ld, int cols,
-                                           float bias) {
+__device__ __forceinline__ void finish_cols(const LinearEpi &e, const float *acc, const T (&res)[CN], int64_t m0, int n,
+                                            int ld, int cols, float bias) {
     const int64_t at = m0 * ld + n;
-    T *out = static_cast<T *>(e.out) + at;
     float v[CN];
 #pragma unroll
     for (int i = 0; i < CN; ++i) v[i] = acc[i];
     if constexpr (FULL) {
-        T res[CN];
-        if (e.residual != nullptr) {
-            const T *p = static_cast<const T *>(e.residual) + at;
-#pragma unroll
-            for (int i = 0; i < CN; ++i) res[i] = p[static_cast<int64_t>(i < cols ? i : 0) * ld];
-        }
 #pragma unroll
         for (int i = 0; i < CN; ++i) v[i] += bias;
         if (e.z_out != nullptr) put_cols<T, CN>(static_cast<T *>(e.z_out) + at, v, ld, cols);
@@ -216,7 +217,15 @@ __device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc,
             for (int i = 0; i < CN; ++i) v[i] += to_f32<T>(res[i]);
         }
     }
-    put_cols<T, CN>(out, v, ld, cols);
+    put_cols<T, CN>(static_cast<T *>(e.out) + at, v, ld, cols);
+}
+
+template <typename T, bool FULL, int CN>
+__device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc, int64_t m0, int n, int ld, int cols,
+                                           float bias) {
+    T res[CN];
+    if (FULL && e.residual != nullptr) get_residual<T, CN>(res, e, m0, n, ld, cols);
+    finish_cols<T, FULL, CN>(e, acc, res, m0, n, ld, cols, bias);
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -482,6 +491,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             const int64_t left = p.M - m0;
             const int rows = left < hm ? static_cast<int>(left > 0 ? left : 0) : hm;
             const float bias = (FULL && p.epi.bias != nullptr && n < p.Nn) ? p.epi.bias[n] : 0.0f;
+            // bf16 with a residual: its values are read 16 columns ahead of their use,
+            // the first before the tile is done (read in place, a 32-column step took
+            // HBM's latency each time)
+            const bool add = FULL && !SPLIT && p.epi.residual != nullptr && n < p.Nn && rows > 0;
+            T res[16];
+            if (add) get_residual<T, 16>(res, p.epi, m0, n, p.Nn, rows);
             float sum[SPLIT ? HMAX : 1];
             const int pieces = SPLIT ? (p.kb + kPieceKb - 1) / kPieceKb : 1;
             for (int pc = 0; pc < pieces; ++pc) {
@@ -505,13 +520,29 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                             sum[c * 16 + j] = pc == 0 ? __uint_as_float(r[j]) : sum[c * 16 + j] + __uint_as_float(r[j]);
                     }
                 } else {
-                    for (int c = 0; c * 32 < rows; ++c) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
-                        tmem_wait_ld();
-                        if (n < p.Nn)
-                            store_cols<T, FULL, 32>(p.epi, reinterpret_cast<const float *>(r), m0 + c * 32, n, p.Nn,
-                                                    rows - c * 32, bias);
+                    if constexpr (FULL) {
+                        for (int c = 0; c * 16 < rows; ++c) {
+                            T next[16];
+                            if (add && c * 16 + 16 < rows)
+                                get_residual<T, 16>(next, p.epi, m0 + c * 16 + 16, n, p.Nn, rows - c * 16 - 16);
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(taddr + c * 16, r);
+                            tmem_wait_ld();
+                            if (n < p.Nn)
+                                finish_cols<T, true, 16>(p.epi, reinterpret_cast<const float *>(r), res, m0 + c * 16, n,
+                                                         p.Nn, rows - c * 16, bias);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) res[j] = next[j];
+                        }
+                    } else {
+                        for (int c = 0; c * 32 < rows; ++c) {
+                            uint32_t r[32];
+                            tmem_ld_32x32b_x32(taddr + c * 32, r);
+                            tmem_wait_ld();
+                            if (n < p.Nn)
+                                store_cols<T, false, 32>(p.epi, reinterpret_cast<const float *>(r), m0 + c * 32, n, p.Nn,
+                                                         rows - c * 32, bias);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -556,6 +587,14 @@ constexpr int kSplitSmem = 216 * 1024;
 
 template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
 
+// One product or two (dW and dx, which share a launch); blocks [0, tiles0 S) are
+// the first's.
+struct SplitArgs {
+    ProdArgs p[2];
+    int tiles0, S, stages;
+    uint64_t timeout_ns;
+};
+
 // Adds the cluster's S <= C parts of columns [j0, j0 + mine) of this lane's n, in
 // rank order, and stores them: 32 loads in flight (loaded one after the other
 // they took 10 us of a 28 us decode product).
@@ -591,14 +630,22 @@ __device__ __forceinline__ void add_parts(const ProdArgs &p, uint32_t at, int S,
 
 template <typename T, int BN>
 __global__ void __launch_bounds__(kSplitThreads, split_ctas(sizeof(T) == 4))
-linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constant__ CUtensorMap tq, const ProdArgs p,
-                    const int S, const int stages, const uint64_t tmo) {
+linear_split_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constant__ CUtensorMap tq0,
+                    const __grid_constant__ CUtensorMap tp1, const __grid_constant__ CUtensorMap tq1,
+                    const __grid_constant__ SplitArgs args) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
     constexpr int COLS = BN < 32 ? 32 : BN;  // tensor-memory columns of one accumulator
     constexpr uint32_t TMEM_COLS = 2 * COLS;
     constexpr uint32_t A_BYTES = 128 * kBK * 2;
     constexpr int kMaxStages = 6;
+    const int S = args.S, stages = args.stages;
+    const uint64_t tmo = args.timeout_ns;
+    int tile = static_cast<int>(blockIdx.x / static_cast<unsigned>(S));
+    const bool second = tile >= args.tiles0;
+    if (second) tile -= args.tiles0;
+    const ProdArgs &p = args.p[second ? 1 : 0];
+    const CUtensorMap *tp = second ? &tp1 : &tp0, *tq = second ? &tq1 : &tq0;
     const uint32_t b_bytes = split_b_bytes<BN>(p.q_mn != 0);
     const uint32_t stage_bytes = PLANES * (A_BYTES + b_bytes);
 
@@ -628,8 +675,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
         mbar_init(drain, 1);
         fence_barrier_init();
         cta_status = 0u;
-        tma_prefetch_desc(&tp);
-        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(tp);
+        tma_prefetch_desc(tq);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&tmem_holder), TMEM_COLS);
@@ -642,15 +689,18 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
     pdl_wait();
 
     const int nt = (p.Nn + 127) / 128;
-    const int64_t tile = blockIdx.x / static_cast<unsigned>(S);
-    const int n0 = static_cast<int>(tile % nt) * 128;
-    const int64_t m0 = tile / nt * BN;
+    const int n0 = tile % nt * 128;
+    const int64_t m0 = static_cast<int64_t>(tile / nt) * BN;
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S);
     const int piece = SPLIT ? kPieceKb : kb1 - kb0;
 
     float sum[BN];
     bool good = true;
+    if (kb0 >= kb1) {  // no share of a short K
+#pragma unroll
+        for (int j = 0; j < BN; ++j) sum[j] = 0.0f;
+    }
     if (warp == 0) {
         const uint32_t one = elect_one();
         int stage = 0, issued = 0;
@@ -670,16 +720,16 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
                     for (int z = 0; z < PLANES; ++z) {
                         const uint32_t a = sa + z * A_BYTES, b = sa + PLANES * A_BYTES + z * b_bytes;
                         if constexpr (decltype(pm)::value) {
-                            load_if(one, a, &tp, fb, n0, kx, z);
-                            load_if(one, a + 8192u, &tp, fb, n0 + 64, kx, z);
+                            load_if(one, a, tp, fb, n0, kx, z);
+                            load_if(one, a + 8192u, tp, fb, n0 + 64, kx, z);
                         } else {
-                            load_if(one, a, &tp, fb, kx, n0, z);
+                            load_if(one, a, tp, fb, kx, n0, z);
                         }
                         if constexpr (decltype(qm)::value) {
-                            load_if(one, b, &tq, fb, mr, kx, z);
-                            if constexpr (BN == 128) load_if(one, b + 8192u, &tq, fb, mr + 64, kx, z);
+                            load_if(one, b, tq, fb, mr, kx, z);
+                            if constexpr (BN == 128) load_if(one, b + 8192u, tq, fb, mr + 64, kx, z);
                         } else {
-                            load_if(one, b, &tq, fb, kx, mr, z);
+                            load_if(one, b, tq, fb, kx, mr, z);
                         }
                     }
                 }
@@ -808,8 +858,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp, const __grid_constan
     } else if (warp >= 2 && good && n < p.Nn) {
         const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
 #pragma unroll
-        for (int c = 0; c < BN / 8; ++c)
-            if (c * 8 < rows) store_cols<T, true, 8>(p.epi, sum + c * 8, m0 + c * 8, n, p.Nn, rows - c * 8, bias);
+        for (int c = 0; c < BN / 16; ++c)
+            if (c * 16 < rows) store_cols<T, true, 16>(p.epi, sum + c * 16, m0 + c * 16, n, p.Nn, rows - c * 16, bias);
     }
     __syncwarp();
     __syncthreads();
@@ -943,22 +993,42 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
 }
 
+int64_t split_tiles(const TcProduct &t, int bn) {
+    return static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + bn - 1) / bn);
+}
+
 template <typename T, int BN>
-cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStream_t s) {
-    const int planes = sizeof(T) == 4 ? 3 : 1;
-    CUtensorMap mp, mq;
-    if (!operand_map(&mp, t.P, planes, t.Nn, t.K, t.p_mn, 128) || !operand_map(&mq, t.Q, planes, t.M, t.K, t.q_mn, BN))
-        return cudaErrorInvalidValue;
-    const ProdArgs p = prod_args(t);
-    const int stage_bytes = planes * (128 * kBK * 2 + split_b_bytes<BN>(t.q_mn));
-    int stages = (kSplitSmem / split_ctas(sizeof(T) == 4) - 1024) / stage_bytes;
-    if (stages > 6) stages = 6;
-    const int smem = 1024 + (stages * stage_bytes > BN * 512 ? stages * stage_bytes : BN * 512);
+cudaError_t launch_split(const TcProduct *t, int count, int S, uint64_t timeout_ns, cudaStream_t s) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr int PLANES = SPLIT ? 3 : 1;
+    CUtensorMap mp[2], mq[2];
+    SplitArgs a{};
+    int stage_bytes = 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+        if (!operand_map(&mp[i], t[i].P, PLANES, t[i].Nn, t[i].K, t[i].p_mn, 128) ||
+            !operand_map(&mq[i], t[i].Q, PLANES, t[i].M, t[i].K, t[i].q_mn, BN))
+            return cudaErrorInvalidValue;
+        a.p[i] = prod_args(t[i]);
+        const int b = PLANES * (128 * kBK * 2 + split_b_bytes<BN>(t[i].q_mn));
+        if (b > stage_bytes) stage_bytes = b;
+        tiles += split_tiles(t[i], BN);
+        if (i == 0) a.tiles0 = static_cast<int>(tiles);
+    }
+    if (count == 1) {
+        mp[1] = mp[0];
+        mq[1] = mq[0];
+    }
+    if (tiles * S > INT32_MAX) return cudaErrorInvalidValue;
+    a.S = S;
+    a.stages = (kSplitSmem / split_ctas(SPLIT) - 1024) / stage_bytes;
+    if (a.stages > 6) a.stages = 6;
+    a.timeout_ns = timeout_ns;
+    const int ring = a.stages * stage_bytes;
+    const int smem = 1024 + (ring > BN * 512 ? ring : BN * 512);
     auto kern = linear_split_kernel<T, BN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + BN - 1) / BN);
-    if (tiles * S > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
     cfg.blockDim = dim3(kSplitThreads);
@@ -973,7 +1043,7 @@ cudaError_t launch_split(const TcProduct &t, int S, uint64_t timeout_ns, cudaStr
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, mp, mq, p, S, stages, timeout_ns);
+    return cudaLaunchKernelEx(&cfg, kern, mp[0], mq[0], mp[1], mq[1], a);
 }
 
 // Whether a product has tiles enough to run on CTA pairs.
@@ -982,20 +1052,40 @@ bool use_pairs(const TcProduct &t, bool fp32, int num_sms) {
     return p.units[0] * 2 >= num_sms / 2;
 }
 
+// One or two products on the split kernel.  BN is the batch rounded up; with
+// many rows it shrinks from 128 as long as not every SM has a CTA.  S: two K
+// blocks a CTA at least.
 template <typename T>
-cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
-    const int bn = t.M <= 16 ? 16 : t.M <= 32 ? 32 : t.M <= 64 ? 64 : 128;
-    const int64_t tiles = static_cast<int64_t>((t.Nn + 127) / 128) * ((t.M + bn - 1) / bn);
-    const int kb = (t.K + kBK - 1) / kBK;
-    int S = static_cast<int>(split_ctas(sizeof(T) == 4) * num_sms / tiles);
-    if (S > 8) S = 8;
-    if (S > kb / 2) S = kb / 2;  // two K blocks a CTA at least
+cudaError_t run_split(const TcProduct *t, int count, uint64_t timeout_ns, int num_sms, cudaStream_t s) {
+    int64_t rows = 0;
+    int kb = 0;
+    for (int i = 0; i < count; ++i) {
+        if (t[i].M > rows) rows = t[i].M;
+        if ((t[i].K + kBK - 1) / kBK > kb) kb = (t[i].K + kBK - 1) / kBK;
+    }
+    const int max_split = kb / 2 > 8 ? 8 : kb / 2 < 1 ? 1 : kb / 2;
+    auto tiles = [&](int bn) {
+        int64_t n = 0;
+        for (int i = 0; i < count; ++i) n += split_tiles(t[i], bn);
+        return n;
+    };
+    int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    while (bn > 32 && tiles(bn) * max_split < num_sms) bn /= 2;
+    int S = static_cast<int>(split_ctas(sizeof(T) == 4) * num_sms / tiles(bn));
+    if (S > max_split) S = max_split;
     if (S < 1) S = 1;
+    // planned for both, so that a gradient's bits do not depend on what else is wanted
+    if (t[0].epi.out == nullptr) {
+        ++t;
+        --count;
+    }
+    if (count == 2 && t[1].epi.out == nullptr) --count;
+    if (count == 0 || t[0].epi.out == nullptr) return cudaSuccess;
     switch (bn) {
-    case 16: return launch_split<T, 16>(t, S, timeout_ns, s);
-    case 32: return launch_split<T, 32>(t, S, timeout_ns, s);
-    case 64: return launch_split<T, 64>(t, S, timeout_ns, s);
-    default: return launch_split<T, 128>(t, S, timeout_ns, s);
+    case 16: return launch_split<T, 16>(t, count, S, timeout_ns, s);
+    case 32: return launch_split<T, 32>(t, count, S, timeout_ns, s);
+    case 64: return launch_split<T, 64>(t, count, S, timeout_ns, s);
+    default: return launch_split<T, 128>(t, count, S, timeout_ns, s);
     }
 }
 
@@ -1003,22 +1093,27 @@ cudaError_t run_split(const TcProduct &t, uint64_t timeout_ns, int num_sms, cuda
 
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s) {
-    bool pairs = true;
-    for (int i = 0; i < count; ++i) pairs = pairs && use_pairs(t[i], fp32, num_sms);
-    if (pairs) {
-        if (fp32)
-            return full ? launch_pair<float, true>(t, count, timeout_ns, num_sms, s)
-                        : launch_pair<float, false>(t, count, timeout_ns, num_sms, s);
-        return full ? launch_pair<__nv_bfloat16, true>(t, count, timeout_ns, num_sms, s)
-                    : launch_pair<__nv_bfloat16, false>(t, count, timeout_ns, num_sms, s);
+    // products of one kind share a launch
+    const bool first = use_pairs(t[0], fp32, num_sms);
+    if (count == 2 && use_pairs(t[1], fp32, num_sms) != first) {
+        cudaError_t e = launch_tc_products(t, 1, fp32, full, timeout_ns, num_sms, s);
+        return e != cudaSuccess ? e : launch_tc_products(t + 1, 1, fp32, full, timeout_ns, num_sms, s);
     }
-    for (int i = 0; i < count; ++i) {
-        cudaError_t e;
-        if (use_pairs(t[i], fp32, num_sms)) e = launch_tc_products(t + i, 1, fp32, full, timeout_ns, num_sms, s);
-        else e = fp32 ? run_split<float>(t[i], timeout_ns, num_sms, s) : run_split<__nv_bfloat16>(t[i], timeout_ns, num_sms, s);
-        if (e != cudaSuccess) return e;
+    if (!first)
+        return fp32 ? run_split<float>(t, count, timeout_ns, num_sms, s)
+                    : run_split<__nv_bfloat16>(t, count, timeout_ns, num_sms, s);
+    // a tile's height does not change a sum's order, so a product alone is planned alone
+    if (t[0].epi.out == nullptr) {
+        ++t;
+        --count;
     }
-    return cudaSuccess;
+    if (count == 2 && t[1].epi.out == nullptr) --count;
+    if (count == 0 || t[0].epi.out == nullptr) return cudaSuccess;
+    if (fp32)
+        return full ? launch_pair<float, true>(t, count, timeout_ns, num_sms, s)
+                    : launch_pair<float, false>(t, count, timeout_ns, num_sms, s);
+    return full ? launch_pair<__nv_bfloat16, true>(t, count, timeout_ns, num_sms, s)
+                : launch_pair<__nv_bfloat16, false>(t, count, timeout_ns, num_sms, s);
 }
 
 }  // namespace moe

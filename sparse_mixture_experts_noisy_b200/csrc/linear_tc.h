@@ -21,7 +21,9 @@ struct TcProduct {
     LinearEpi epi;
 };
 
-// One product, or two that share a launch where both have tiles enough.
+// One product, or two that share a launch where they run on the same kernel.  A
+// product whose out is null is not computed, but counts in the choice of the
+// other's K split.
 // full: bias, activation, residual and z of the epilogue; else out alone.
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s);
