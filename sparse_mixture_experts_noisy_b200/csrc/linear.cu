@@ -93,12 +93,12 @@ linear_pack_kernel(const T *__restrict__ in0, int64_t rows0, __nv_bfloat16 *out0
 // dZ = dy act'(z), rounded to the storage type and laid out as an operand, and
 // the column sums of the unrounded dZ over a chunk of rows.  A block takes 256
 // columns, eight to a lane, its 8 warps every eighth row of the chunk, ROWS at a
-// time.  dz and part nullable.  O: bf16 for an operand (fp32 in parts), or T
-// with ld = n for the CUDA-core products.
-template <typename T, typename O>
+// time.  operand (rows of ld, fp32 in parts), plain (rows of n in the storage
+// type, for the CUDA-core products) and part are nullable.
+template <typename T>
 __global__ void __launch_bounds__(256, 2)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
-                 int64_t chunk_rows, O *dz, float *part) {
+                 int64_t chunk_rows, __nv_bfloat16 *operand, T *plain, float *part) {
     constexpr int ROWS = sizeof(T) == 4 ? 2 : 4;  // rows a lane has in flight
     __shared__ float red[8][8][33];
     pdl_trigger();
@@ -136,14 +136,11 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) a[i] += v[i];
-                if (dz != nullptr) {
-                    if (sizeof(O) == 4 || (sizeof(T) == 2 && ld % 8 != 0)) {  // plain rows for the CUDA cores
+                if (operand != nullptr) put_operand8<T>(operand, q * ld + c, M * ld, v);
+                if (plain != nullptr) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c + i < n) dz[q * ld + c + i] = from_f32<O>(v[i]);
-                    } else {
-                        put_operand8<T>(reinterpret_cast<__nv_bfloat16 *>(dz), q * ld + c, M * ld, v);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < n) plain[q * n + c + i] = from_f32<T>(v[i]);
                 }
             }
         }
@@ -219,10 +216,13 @@ cudaError_t pack(const void *&in0, int64_t rows0, void *out0, const void *&in1, 
     return e;
 }
 
-// A few tokens: the CUDA-core kernels, unless W is already an operand, which
-// streams as fast through the tensor cores (dW has no such form).
+// A few tokens: the CUDA-core kernels, unless W is an operand as it is, which
+// streams as fast through the tensor cores.  For fp32 they save a copy of W in
+// parts, 2.5 times its bytes.
 bool use_skinny(int64_t M, int dt, int cols) { return M <= kSkinnyRows && needs_pack(dt, cols); }
-bool use_skinny_dw(int64_t M) { return M <= kSkinnyRows; }
+// dW has no weights to copy, and its CUDA-core kernel is bound by arithmetic past
+// a few tokens: bf16 9200 x 11200 from 6 tokens 76 us, from 16 at 4096 x 14336
+// 121 us, where the tensor cores take about 35: kSkinnyDwRows.
 
 struct FwdScratch {
     size_t x, W, total;
@@ -235,34 +235,36 @@ FwdScratch fwd_scratch(int64_t M, int d_in, int d_out, int dt) {
     return L;
 }
 
-// What a backward call's products read: dZ as rows of the storage type for the
-// CUDA-core kernels, as an operand for the tensor cores (never both).
+// Kernels of a backward call's products, and the forms of dZ they read that have
+// to be written: plain rows (CUDA cores) and an operand (tensor cores).  bf16 rows
+// of a multiple of 8 elements are both.
 struct BwdWays {
     bool dx_skinny, dw_skinny;
-    bool dz_rows, dz_operand;  // dZ is written to scratch in this form
+    bool plain, operand;
 };
 BwdWays bwd_ways(int64_t M, int d_in, int d_out, int dt, int act) {
     BwdWays w{};
-    w.dw_skinny = use_skinny_dw(M);
-    w.dx_skinny = w.dw_skinny && (use_skinny(M, dt, d_in) || needs_pack(dt, d_out));
-    // rows are an operand already when bf16 and a multiple of 8 wide
-    w.dz_rows = w.dw_skinny && act != kActNone;
-    w.dz_operand = !w.dw_skinny && (act != kActNone || needs_pack(dt, d_out));
+    w.dw_skinny = M <= kSkinnyDwRows;
+    w.dx_skinny = use_skinny(M, dt, d_in) || use_skinny(M, dt, d_out);
+    const bool tc = !w.dw_skinny || !w.dx_skinny, same = !needs_pack(dt, d_out);
+    w.operand = tc && (act != kActNone || !same);
+    w.plain = (w.dw_skinny || w.dx_skinny) && act != kActNone && !(w.operand && same);
     return w;
 }
 
-// Byte offsets inside the backward workspace: dZ, x and W as operands, and the
-// row chunks' partial sums of db.
+// Byte offsets inside the backward workspace: dZ in both forms, x and W as
+// operands, and the row chunks' partial sums of db.
 struct BwdScratch {
-    size_t dz, x, W, part, total;
+    size_t operand, plain, x, W, part, total;
 };
 BwdScratch bwd_scratch(int64_t M, int d_in, int d_out, int dt, int act) {
     const BwdWays w = bwd_ways(M, d_in, d_out, dt, act);
     BwdScratch L{};
     size_t o = 0;
-    L.dz = o;
-    if (w.dz_rows) o += align_up(static_cast<size_t>(M) * d_out * (dt == 1 ? 2 : 4), 256);
-    if (w.dz_operand) o += operand_bytes(M, d_out, dt);
+    L.operand = o;
+    if (w.operand) o += operand_bytes(M, d_out, dt);
+    L.plain = o;
+    if (w.plain) o += align_up(static_cast<size_t>(M) * d_out * (dt == 1 ? 2 : 4), 256);
     L.x = o;
     if (!w.dw_skinny && needs_pack(dt, d_in)) o += operand_bytes(M, d_in, dt);
     L.W = o;
@@ -317,21 +319,21 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         using T = decltype(tag);
         cudaError_t e = cudaSuccess;
         const bool products = a.dx != nullptr || a.dW != nullptr;
-        const bool rows = products && ways.dz_rows, operand = products && ways.dz_operand;
-        float *part = a.db != nullptr ? reinterpret_cast<float *>(w + L.part) : nullptr;
+        const int ld = pad8(a.d_out);
         const int64_t chunks = row_chunks(a.M, a.d_out);
-        const void *dz = rows || operand ? static_cast<const void *>(w + L.dz) : a.dy;
-        if (rows || operand || part != nullptr) {
-            const int ld = operand ? pad8(a.d_out) : a.d_out;
+        __nv_bfloat16 *operand = products && ways.operand ? reinterpret_cast<__nv_bfloat16 *>(w + L.operand) : nullptr;
+        T *plain = products && ways.plain ? reinterpret_cast<T *>(w + L.plain) : nullptr;
+        float *part = a.db != nullptr ? reinterpret_cast<float *>(w + L.part) : nullptr;
+        // what the products read: dy itself where no dZ of that form is written
+        const void *dz_operand = operand != nullptr ? static_cast<const void *>(operand) : a.dy;
+        const T *dz_plain = plain != nullptr ? plain
+                            : (operand != nullptr && a.act != kActNone) ? reinterpret_cast<const T *>(operand)
+                                                                        : static_cast<const T *>(a.dy);
+        if (operand != nullptr || plain != nullptr || part != nullptr) {
             const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(ld) + 255) / 256), static_cast<unsigned>(chunks));
-            auto dz_pass = [&](auto out) {
-                using O = decltype(out);
-                return launch_pdl(linear_dz_kernel<T, O>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
-                                  static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks,
-                                  rows || operand ? reinterpret_cast<O *>(w + L.dz) : static_cast<O *>(nullptr),
-                                  chunks == 1 ? a.db : part);
-            };
-            e = rows ? dz_pass(T{}) : dz_pass(__nv_bfloat16{});
+            e = launch_pdl(linear_dz_kernel<T>, grid, dim3(256), 0, s, static_cast<const T *>(a.dy),
+                           static_cast<const T *>(a.z), a.act, a.M, a.d_out, ld, (a.M + chunks - 1) / chunks, operand,
+                           plain, chunks == 1 ? a.db : part);
             if (e != cudaSuccess) return e;
         }
         if (part != nullptr && chunks > 1) {
@@ -349,20 +351,20 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
         TcProduct t[2];
         int n = 0;
         if (!ways.dw_skinny)
-            t[n++] = TcProduct{x, dz, a.d_out, a.d_in, static_cast<int>(a.M), true, true, {nullptr, kActNone, nullptr, a.dW, nullptr}};
+            t[n++] = TcProduct{x, dz_operand, a.d_out, a.d_in, static_cast<int>(a.M), true, true, {nullptr, kActNone, nullptr, a.dW, nullptr}};
         if (!ways.dx_skinny)
-            t[n++] = TcProduct{W, dz, a.M, a.d_in, a.d_out, true, false, {nullptr, kActNone, nullptr, a.dx, nullptr}};
+            t[n++] = TcProduct{W, dz_operand, a.M, a.d_in, a.d_out, true, false, {nullptr, kActNone, nullptr, a.dx, nullptr}};
         if (n > 0) {
             e = launch_tc_products(t, n, sizeof(T) == 4, false, timeout_ns, num_sms, s);
             if (e != cudaSuccess) return e;
         }
         if (a.dx != nullptr && ways.dx_skinny) {
-            e = launch_skinny_dx<T>(static_cast<const T *>(dz), static_cast<const T *>(a.W), a.M, a.d_in, a.d_out,
+            e = launch_skinny_dx<T>(dz_plain, static_cast<const T *>(a.W), a.M, a.d_in, a.d_out,
                                     static_cast<T *>(a.dx), s);
             if (e != cudaSuccess) return e;
         }
         if (a.dW != nullptr && ways.dw_skinny)
-            e = launch_skinny_dw<T>(static_cast<const T *>(dz), static_cast<const T *>(a.x), a.M, a.d_in, a.d_out,
+            e = launch_skinny_dw<T>(dz_plain, static_cast<const T *>(a.x), a.M, a.d_in, a.d_out,
                                     static_cast<T *>(a.dW), s);
         return e;
     };

@@ -19,17 +19,17 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = to_f32<T>(*p);
-    } else {
-        const uint4 raw = *reinterpret_cast<const uint4 *>(p);
-        const T *e = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_f32<T>(e[i]);
-    }
-}
+// VEC elements as they lie in memory.
+template <typename T, int VEC> struct Raw {
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ float operator[](int i) const { return to_f32<T>(reinterpret_cast<const T *>(&u)[i]); }
+};
+template <typename T> struct Raw<T, 1> {
+    T u;
+    __device__ __forceinline__ void load(const T *p) { u = *p; }
+    __device__ __forceinline__ float operator[](int) const { return to_f32<T>(u); }
+};
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
@@ -83,21 +83,23 @@ skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K
     const int n0 = (blockIdx.x * GROUPS + grp) * R;
     float acc[V] = {};  // [r][m]
     if (n0 < Nn) {
-        for (int k = (warp % KW * 32 + lane) * VEC; k < K; k += KW * 32 * VEC) {
-            float w[R][VEC];
+        // rows past W's or x's last read a valid one; their sums are dropped
+        const T *wr[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                load_vec<T, VEC>(W + static_cast<int64_t>(n0 + r < Nn ? n0 + r : n0) * K + k, w[r]);
+        for (int r = 0; r < R; ++r) wr[r] = W + static_cast<int64_t>(n0 + r < Nn ? n0 + r : n0) * K;
+#pragma unroll 2
+        for (int k = (warp % KW * 32 + lane) * VEC; k < K; k += KW * 32 * VEC) {
+            Raw<T, VEC> w[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[r].load(wr[r] + k);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (m < M) {
-                    float a[VEC];
-                    load_vec<T, VEC>(x + static_cast<int64_t>(m) * K + k, a);
+                Raw<T, VEC> a;
+                a.load(x + static_cast<int64_t>(m < M ? m : 0) * K + k);
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) acc[r * MT + m] = fmaf(a[i], w[r][i], acc[r * MT + m]);
-                }
+                    for (int i = 0; i < VEC; ++i) acc[r * MT + m] = fmaf(a[i], w[r][i], acc[r * MT + m]);
             }
         }
     }
@@ -126,35 +128,41 @@ skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K
 template <typename T, int VEC, int MT>
 __global__ void __launch_bounds__(kThreads)
 skinny_dx_kernel(const T *__restrict__ dz, const T *__restrict__ W, int M, int Ni, int No, int S, T *dx) {
-    constexpr int COLS = 32 * VEC, CHUNK = 64;  // rows of W a chunk: 8 a warp
-    extern __shared__ float smem[];             // [kWarps][MT][COLS]
-    __shared__ float g[CHUNK][MT];              // dZ of the chunk
+    constexpr int COLS = 32 * VEC, CHUNK = 128, FLY = 8;  // rows of W a chunk; a lane's loads in flight
+    extern __shared__ float smem[];                       // [kWarps][MT][COLS]
+    __shared__ __align__(16) float g[CHUNK][MT];          // dZ of the chunk
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int i0 = blockIdx.x / S * COLS, col = i0 + lane * VEC;
+    const bool live = col < Ni;
     float acc[MT][VEC] = {};
     for (int base = rank * CHUNK; base < No; base += S * CHUNK) {
+        // the chunk's first rows are on their way while its dZ is staged
+        Raw<T, VEC> w[FLY];
+        auto fetch = [&](int first) {
+#pragma unroll
+            for (int u = 0; u < FLY; ++u) {
+                const int o = base + warp + 8 * (first + u);
+                if (live) w[u].load(W + static_cast<int64_t>(o < No ? o : base) * Ni + col);
+            }
+        };
+        fetch(0);
         __syncthreads();
         for (int q = threadIdx.x; q < CHUNK * MT; q += kThreads) {
             const int m = q / CHUNK, o = q % CHUNK;
             g[o][m] = (m < M && base + o < No) ? to_f32<T>(dz[static_cast<int64_t>(m) * No + base + o]) : 0.0f;
         }
         __syncthreads();
-        if (col < Ni) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float w[4][VEC];
+        for (int f = 0; f < CHUNK / kWarps; f += FLY) {
+            if (f > 0) fetch(f);
+            if (live) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int o = base + warp + 8 * (4 * h + u);
-                    load_vec<T, VEC>(W + static_cast<int64_t>(o < No ? o : base) * Ni + col, w[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int o = warp + 8 * (4 * h + u);
-                    if (base + o < No) {
+                for (int u = 0; u < FLY; ++u) {
+                    const int o = warp + 8 * (f + u);
+                    if (base + o < No) {  // a row past the last would bring its own NaN
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -209,7 +217,7 @@ template <typename T, int VEC, int MT>
 __global__ void __launch_bounds__(kThreads)
 skinny_dw_kernel(const T *__restrict__ dz, const T *__restrict__ x, int M, int Ni, int No, T *dW) {
     constexpr int ROWS = 64;
-    __shared__ float g[ROWS][MT];
+    __shared__ __align__(16) float g[ROWS][MT];
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,7 +227,12 @@ skinny_dw_kernel(const T *__restrict__ dz, const T *__restrict__ x, int M, int N
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) a[m][i] = 0.0f;
-        if (m < M && col < Ni) load_vec<T, VEC>(x + static_cast<int64_t>(m) * Ni + col, a[m]);
+        if (m < M && col < Ni) {
+            Raw<T, VEC> raw;
+            raw.load(x + static_cast<int64_t>(m) * Ni + col);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) a[m][i] = raw[i];
+        }
     }
     for (int64_t o0 = static_cast<int64_t>(blockIdx.y) * ROWS; o0 < No; o0 += static_cast<int64_t>(gridDim.y) * ROWS) {
         __syncthreads();
@@ -248,12 +261,15 @@ template <int V> struct Int {
 };
 
 // f(tag of VEC, tag of MT) for rows of `cols` elements.
-template <typename T, typename F> cudaError_t skinny_pick(int cols, int64_t M, F f) {
+template <typename T, int MOST, typename F> cudaError_t skinny_pick(int cols, int64_t M, F f) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     auto with = [&](auto vec) {
         if (M <= 1) return f(vec, Int<1>{});
-        if (M <= 4) return f(vec, Int<4>{});
-        return f(vec, Int<kSkinnyRows>{});
+        if constexpr (MOST > 4) {
+            if (M > 8) return f(vec, Int<MOST>{});
+            if (M > 4) return f(vec, Int<8>{});
+        }
+        return f(vec, Int<4>{});
     };
     return cols % VEC == 0 ? with(Int<VEC>{}) : with(Int<1>{});
 }
@@ -262,7 +278,7 @@ template <typename T, typename F> cudaError_t skinny_pick(int cols, int64_t M, F
 
 template <typename T>
 cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, const LinearEpi &epi, cudaStream_t s) {
-    return skinny_pick<T>(K, M, [&](auto vec, auto mt) {
+    return skinny_pick<T, kSkinnyRows>(K, M, [&](auto vec, auto mt) {
         // rows a warp group: enough to share x, few enough that the SMs have blocks.  A
         // group is a warp where a row gives it work for four vectors a lane.
         constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
@@ -278,14 +294,14 @@ cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, 
 
 template <typename T>
 cudaError_t launch_skinny_dx(const T *dz, const T *W, int64_t M, int Ni, int No, T *dx, cudaStream_t s) {
-    return skinny_pick<T>(Ni, M, [&](auto vec, auto mt) {
+    return skinny_pick<T, kSkinnyRows>(Ni, M, [&](auto vec, auto mt) {
         constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
         constexpr int smem = kWarps * MT * 32 * V * static_cast<int>(sizeof(float));
         auto kern = skinny_dx_kernel<T, V, MT>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int tiles = (Ni + 32 * V - 1) / (32 * V);
-        int S = (No + 63) / 64;  // a chunk of rows each at least
+        int S = (No + 127) / 128;  // a chunk of rows each at least
         if (S > 8) S = 8;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
@@ -307,7 +323,7 @@ cudaError_t launch_skinny_dx(const T *dz, const T *W, int64_t M, int Ni, int No,
 
 template <typename T>
 cudaError_t launch_skinny_dw(const T *dz, const T *x, int64_t M, int Ni, int No, T *dW, cudaStream_t s) {
-    return skinny_pick<T>(Ni, M, [&](auto vec, auto mt) {
+    return skinny_pick<T, kSkinnyDwRows>(Ni, M, [&](auto vec, auto mt) {
         constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
         const int64_t gy = (static_cast<int64_t>(No) + 63) / 64;
         return launch_pdl(skinny_dw_kernel<T, V, MT>,

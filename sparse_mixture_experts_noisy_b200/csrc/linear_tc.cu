@@ -174,6 +174,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 // this lane's n.  FULL: bias, activation, residual and z as the epilogue says;
 // otherwise the value alone.  Every choice is made once for the CN columns: a
 // branch per element made a 256 x 256 tile's epilogue take 20 us.
+// Measured and not kept, at 64 x 4096 -> 14336 (dW, 40 us) and 4096 x 256 -> 4096
+// (24 us): two elements a lane by a swap between neighbouring lanes, 44 and 27 us;
+// the next columns read from tensor memory while these are stored, with the loop
+// unrolled for it, 40 and 29 us (more instructions to fetch).
 template <typename T, int CN>
 __device__ __forceinline__ void put_cols(T *p, const float (&v)[CN], int ld, int cols) {
     if (cols >= CN) {
@@ -265,8 +269,7 @@ struct PairUnit {
     int64_t m0;
 };
 
-__device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npairs, int i, PairUnit &t) {
-    const int n1 = pair < a.units[0] ? (a.units[0] - pair + npairs - 1) / npairs : 0;
+__device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npairs, int n1, int i, PairUnit &t) {
     int u;
     if (i < n1) {
         t.prob = 0;
@@ -313,6 +316,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int n1 = pair < args.units[0] ? (args.units[0] - pair + npairs - 1) / npairs : 0;  // units of the first product
     uint32_t *status = &cta_status;
     const uint64_t tmo = args.timeout_ns;
     const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
@@ -354,7 +358,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         uint32_t phase = 0;
         bool ok = true;
         PairUnit t;
-        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+        for (int i = 0; ok && pair_unit(args, pair, npairs, n1, i, t); ++i) {
             const CUtensorMap *tp = t.prob ? &tp1 : &tp0, *tq = t.prob ? &tq1 : &tq0;
             const int nr = t.n0 + static_cast<int>(rank) * 128;
             const int qr = args.p[t.prob].tm / 2, mr = static_cast<int>(t.m0) + static_cast<int>(rank) * qr;
@@ -418,7 +422,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             uint32_t phase = 0;
             bool ok = true, any = false;
             PairUnit t;
-            for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+            for (int i = 0; ok && pair_unit(args, pair, npairs, n1, i, t); ++i) {
                 const int kbs = args.p[t.prob].kb;
                 by_layout(args.p[t.prob].p_mn != 0, args.p[t.prob].q_mn != 0, [&](auto pm, auto qm) {
                     constexpr bool PM = decltype(pm)::value, QM = decltype(qm)::value;
@@ -483,7 +487,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         int local = 0;
         bool ok = true;
         PairUnit t;
-        for (int i = 0; ok && pair_unit(args, pair, npairs, i, t); ++i) {
+        for (int i = 0; ok && pair_unit(args, pair, npairs, n1, i, t); ++i) {
             const ProdArgs &p = args.p[t.prob];
             const int n = t.n0 + static_cast<int>(rank) * 128 + q * 32 + lane;
             const int hm = p.tm / 2;  // m of this group
