@@ -46,7 +46,11 @@ cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
 namespace {
 
 constexpr int kBK = 64;        // K elements per stage: 128 bytes, one swizzle row
-constexpr int kPieceKb = 4;    // K blocks per piece of an fp32 product
+// K blocks per piece of an fp32 product.  2-norm of the error over the result's at
+// 4000 x 4096 x 4096, and the time of 4096^3: 1 block 1.7e-7 and 729 us (the
+// epilogue warps cannot keep up), 2 blocks 6.0e-7 and 580, 4 blocks 1.5e-6 and 575;
+// an fp32 product on CUDA cores has 1.1e-6.
+constexpr int kPieceKb = 2;
 constexpr int kTerms = 6;      // products of parts
 
 // Plane of P and of Q for term t: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).

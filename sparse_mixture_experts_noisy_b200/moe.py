@@ -656,6 +656,72 @@ class MoELayer:
                            b_up=self.b_up, b_down=self.b_down)
 
 
+class MoEBlock:
+    """The feed-forward half of a transformer block around the layer
+    ("nanoMoEの深層解剖" slide 4: the MoE layer + normalization), pre-norm, with
+    an optional shared expert: a dense FFN that every token passes beside the
+    routed ones.
+        h = x + delta,  n = LayerNorm(h)
+        s = h + W2 act(W1 n + b1) + b2   (h itself without a shared expert)
+        m = MoE(n)
+    __call__ returns (s, m), the residual stream and the branch still to be added
+    to it, which is the next block's (x, delta): the adds cost no pass of their
+    own.  After the last block, moe_layer_norm(s, ..., residual=m).
+
+    gamma, beta: [d] fp32 (None: 1, 0).  shared: (W1 [d_s, d], b1, W2 [d, d_s],
+    b2), the biases fp32 or None.  Runs on the current stream."""
+
+    def __init__(self, layer: MoELayer, gamma=None, beta=None, eps=1e-5, shared=None, shared_act=ACT_RELU):
+        self.layer, self.gamma, self.beta, self.eps = layer, gamma, beta, float(eps)
+        self.shared, self.shared_act = shared, int(shared_act)
+
+    def __call__(self, x, delta=None, noise=None):
+        n, h, _, _ = moe_layer_norm(x, self.gamma, self.beta, self.eps, residual=delta)
+        m = self.layer(n, noise=noise)
+        if self.shared is None:
+            return h, m
+        W1, b1, W2, b2 = self.shared
+        u = moe_linear(n, W1, b=b1, act=self.shared_act)
+        return moe_linear(u, W2, b=b2, residual=h), m
+
+    def train(self, x, delta=None, noise=None):
+        """__call__ that keeps what backward() needs -> (s, m, saved).  The
+        layer's experts must be ReLU without biases (moe_expert_ffn_train)."""
+        L = self.layer
+        if L.act != ACT_RELU or L.b_up is not None or L.b_down is not None:
+            raise ValueError("training needs ReLU experts without biases")
+        n, h, mean, rstd = moe_layer_norm(x, self.gamma, self.beta, self.eps, residual=delta, want_stats=True)
+        topk, gates, _ = moe_route(n, L.W_g, L.k, b_g=L.b_g, noise=noise, sigma=L.sigma, want_logits=False)
+        d = moe_dispatch(topk, n, L.E, L.cf)
+        out, H = moe_expert_ffn_train(d["x_gathered"], d["offsets"], d["counts"], L.W_up, L.W_down)
+        m = moe_combine(out, d["slot"], topk, d["offsets"], gates)
+        s = h
+        saved = dict(n=n, h=h, mean=mean, rstd=rstd, topk=topk, gates=gates, dispatch=d, out=out, H=H)
+        if self.shared is not None:
+            W1, b1, W2, b2 = self.shared
+            saved["u"], saved["z"] = moe_linear(n, W1, b=b1, act=self.shared_act, keep_z=True)
+            s = moe_linear(saved["u"], W2, b=b2, residual=h)
+        return s, m, saved
+
+    def backward(self, ds, dm, saved):
+        """Gradients for those of s and m -> dict(dx (of x and delta alike),
+        dgamma, dbeta, dW_g, db_g, dW_up, dW_down, and with a shared expert dW1,
+        db1, dW2, db2)."""
+        L, v, d = self.layer, saved, saved["dispatch"]
+        g = moe_backward(v["n"], L.W_g, L.W_up, L.W_down, L.k, v["topk"], v["gates"], d["slot"], d["offsets"],
+                         d["counts"], d["x_gathered"], v["H"], v["out"], dm)
+        dn = g.pop("dx")
+        g.pop("ws")
+        if self.shared is not None:
+            W1, _, W2, _ = self.shared
+            second = moe_linear_backward(ds, v["u"], W2)
+            first = moe_linear_backward(second["dx"], v["n"], W1, act=self.shared_act, z=v["z"])
+            g.update(dW1=first["dW"], db1=first["db"], dW2=second["dW"], db2=second["db"])
+            dn = dn.add_(first["dx"])
+        g.update(moe_layer_norm_backward(dn, v["h"], v["mean"], v["rstd"], gamma=self.gamma, dres=ds, dx=dn))
+        return g
+
+
 class GraphedForward:
     """moe_forward captured once in a CUDA graph over static buffers.
 
