@@ -196,9 +196,8 @@ template <int LEFT> __device__ __forceinline__ void copy_wait() {
 // elements a lane needs up to 190 registers in the backward: 256 threads.
 template <int TPR, int EPT> struct NormCfg {
     static constexpr bool LONG = TPR == 32 && EPT > 16;
-    static constexpr bool HOLD = TPR == 32 || EPT <= 16;  // gamma, beta, column sums in registers
-    static constexpr int FWD_THREADS = LONG ? 256 : 512, FWD_PER_SM = (LONG || EPT == 8) ? 2 : 1;
-    static constexpr int BWD_THREADS = LONG ? 256 : 512;
+    static constexpr bool HOLD = TPR < 512 || EPT <= 16;  // gamma, beta, column sums in registers
+    static constexpr int THREADS = LONG ? 256 : 512, FWD_PER_SM = (LONG || EPT == 8) ? 2 : 1;
 };
 // Rows on their way: six, or as many as `budget` bytes of shared memory hold.
 // The budget is what keeps HBM busy, 64 KB an SM of forward rows and 112 KB of
@@ -208,11 +207,11 @@ constexpr int ring_depth(int arrays, int ch, int threads, int budget) {
     const int n = budget / (arrays * ch * threads * 16);
     return n > 6 ? 6 : n < 1 ? 1 : n;
 }
-template <int TPR, int EPT> constexpr int fwd_depth(int ch) {
-    return ring_depth(2, ch, NormCfg<TPR, EPT>::FWD_THREADS, 64 * 1024 / NormCfg<TPR, EPT>::FWD_PER_SM);
+template <int TPR, int EPT> constexpr int fwd_depth(int arrays, int ch) {
+    return ring_depth(arrays, ch, NormCfg<TPR, EPT>::THREADS, 64 * 1024 / NormCfg<TPR, EPT>::FWD_PER_SM);
 }
-template <int TPR, int EPT> constexpr int bwd_depth(int ch) {
-    return ring_depth(3, ch, NormCfg<TPR, EPT>::BWD_THREADS, 112 * 1024);
+template <int TPR, int EPT> constexpr int bwd_depth(int arrays, int ch) {
+    return ring_depth(arrays, ch, NormCfg<TPR, EPT>::THREADS, 112 * 1024);
 }
 
 template <typename T, int TPR, int CH, bool AL>
@@ -351,8 +350,9 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], float (*red)[NV][32], 
 }
 
 // Rows too wide to HOLD gamma and beta read them again for each row, from the L1 cache.
-template <typename T, int TPR, int CH, bool AL>
-__global__ void __launch_bounds__(NormCfg<TPR, RowLayout<T, TPR, CH, AL>::EPT>::FWD_THREADS,
+// ADD: with a residual.
+template <typename T, int TPR, int CH, bool AL, bool ADD>
+__global__ void __launch_bounds__(NormCfg<TPR, RowLayout<T, TPR, CH, AL>::EPT>::THREADS,
                                   NormCfg<TPR, RowLayout<T, TPR, CH, AL>::EPT>::FWD_PER_SM)
 norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, const float *__restrict__ beta,
                 float eps, int64_t N, int d, int64_t G, T *y, T *sum_out, float *mean_out, float *rstd_out) {
@@ -360,9 +360,10 @@ norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, 
     constexpr int VEC = L::VEC;
     using Cfg = NormCfg<TPR, L::EPT>;
     constexpr bool HOLD = Cfg::HOLD;
-    constexpr int DEPTH = fwd_depth<TPR, L::EPT>(CH), THREADS = Cfg::FWD_THREADS;
+    constexpr uint32_t arrays = ADD ? 2 : 1;
+    constexpr int DEPTH = fwd_depth<TPR, L::EPT>(arrays, CH), THREADS = Cfg::THREADS;
     constexpr uint32_t STEP = THREADS * 16;  // between a thread's slots
-    extern __shared__ uint4 ring[];          // [DEPTH][1 or 2 arrays][CH][THREADS]
+    extern __shared__ uint4 ring[];          // [DEPTH][arrays][CH][THREADS]
     __shared__ float red[2][1][32];
     pdl_trigger();
     const int t = threadIdx.x % TPR;
@@ -370,8 +371,6 @@ norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, 
     pdl_wait();
     if (g >= N) return;
     const L lay(d, AL ? 0 : static_cast<int>((g * d) % VEC), t);
-    const bool add = residual != nullptr;
-    const uint32_t arrays = add ? 2u : 1u;
     const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
     const int64_t total = N * d;
     const float inv_d = 1.0f / static_cast<float>(d);
@@ -379,7 +378,7 @@ norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, 
         if (row < N) {
             const uint32_t s = slot0 + stage * arrays * CH * STEP;
             lay.fetch(x + row * d, total - row * d, s, STEP);
-            if (add) lay.fetch(residual + row * d, total - row * d, s + CH * STEP, STEP);
+            if constexpr (ADD) lay.fetch(residual + row * d, total - row * d, s + CH * STEP, STEP);
         }
         copy_commit();
     };
@@ -405,7 +404,7 @@ norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, 
             const uint4 xr = mine[c * THREADS];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[c][i] = elem<T>(xr, i);
-            if (add) {
+            if constexpr (ADD) {
                 const uint4 rr = mine[(CH + c) * THREADS];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) v[c][i] += elem<T>(rr, i);
@@ -455,19 +454,20 @@ norm_fwd_kernel(const T *x, const T *residual, const float *__restrict__ gamma, 
 // The backward: both row sums in one reduction, and the column sums of the
 // group's rows in registers (HOLD) or, past 16 elements a thread, in shared
 // memory, each thread its own entries.  At the end the block's groups add their
-// columns in order.  part: [grid][2][d], null without column sums.
-template <typename T, int TPR, int CH, bool AL>
-__global__ void __launch_bounds__(NormCfg<TPR, RowLayout<T, TPR, CH, AL>::EPT>::BWD_THREADS)
+// columns in order.  part: [grid][2][d], null without column sums.  ADD: with dres.
+template <typename T, int TPR, int CH, bool AL, bool ADD>
+__global__ void __launch_bounds__(NormCfg<TPR, RowLayout<T, TPR, CH, AL>::EPT>::THREADS)
 norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const float *__restrict__ mean,
                 const float *__restrict__ rstd, const T *dres, int64_t N, int d, int64_t G, int period, T *dx, float *part) {
     using L = RowLayout<T, TPR, CH, AL>;
     constexpr int VEC = L::VEC;
     using Cfg = NormCfg<TPR, L::EPT>;
-    constexpr int DEPTH = bwd_depth<TPR, L::EPT>(CH), THREADS = Cfg::BWD_THREADS, GROUPS = THREADS / TPR;
+    constexpr uint32_t arrays = ADD ? 3 : 2;
+    constexpr int DEPTH = bwd_depth<TPR, L::EPT>(arrays, CH), THREADS = Cfg::THREADS, GROUPS = THREADS / TPR;
     constexpr bool HOLD = Cfg::HOLD;
     static_assert(HOLD || GROUPS == 1, "column sums in shared memory belong to one group");
     constexpr uint32_t STEP = THREADS * 16;
-    extern __shared__ uint4 ring[];  // [DEPTH][2 or 3 arrays][CH][THREADS], then !HOLD: [2][CH][VEC][THREADS] floats
+    extern __shared__ uint4 ring[];  // [DEPTH][arrays][CH][THREADS], then !HOLD: [2][CH][VEC][THREADS] floats
     __shared__ float red[2][2][32];
     pdl_trigger();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -475,8 +475,6 @@ norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const 
     const int P = AL ? 1 : static_cast<int>(period);
     const int64_t g = blockIdx.x % P + static_cast<int64_t>(P) * (static_cast<int64_t>(blockIdx.x / P) * GROUPS + grp);
     const L lay(d, AL ? 0 : static_cast<int>((g * d) % VEC), t);
-    const bool skip = dres != nullptr;
-    const uint32_t arrays = skip ? 3u : 2u;
     const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
     float *cols = reinterpret_cast<float *>(ring + (HOLD ? 0 : DEPTH * arrays * CH * THREADS));
     const int64_t total = N * d;
@@ -495,7 +493,7 @@ norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const 
             const uint32_t s = slot0 + stage * arrays * CH * STEP;
             lay.fetch(dy + row * d, total - row * d, s, STEP);
             lay.fetch(h + row * d, total - row * d, s + CH * STEP, STEP);
-            if (skip) lay.fetch(dres + row * d, total - row * d, s + 2 * CH * STEP, STEP);
+            if constexpr (ADD) lay.fetch(dres + row * d, total - row * d, s + 2 * CH * STEP, STEP);
         }
         copy_commit();
     };
@@ -530,7 +528,7 @@ norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const 
             }
             lay.inside(yv, c);
             lay.inside(xh[c], c);
-            if (skip) dr[c] = mine[(2 * CH + c) * THREADS];
+            if constexpr (ADD) dr[c] = mine[(2 * CH + c) * THREADS];
             float gc[VEC];
             if constexpr (!HOLD) lay.columns(gamma, 1.0f, c, gc);
 #pragma unroll
@@ -556,7 +554,7 @@ norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const 
         }
         group_sum<TPR>(s, red, buf);
         buf ^= 1;
-        if (skip) {
+        if constexpr (ADD) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) asm volatile("" ::"r"(dr[c].x), "r"(dr[c].y), "r"(dr[c].z), "r"(dr[c].w));
         }
@@ -568,7 +566,7 @@ norm_bwd_kernel(const T *dy, const T *h, const float *__restrict__ gamma, const 
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 gy[c][i] = rs_row * (gy[c][i] - ma - xh[c][i] * mb);
-                if (skip) gy[c][i] += elem<T>(dr[c], i);
+                if constexpr (ADD) gy[c][i] += elem<T>(dr[c], i);
             }
             lay.store(dx + base, c, pack<T>(gy[c]));
         }
@@ -617,10 +615,9 @@ constexpr int kNormSms = 148;  // groups are counted for a B200; the bits then d
 // Threads a row and elements a thread for rows of d elements (0: too wide for
 // registers).  A row that starts inside a vector needs up to VEC - 1 more.
 // Few threads a row save reductions and barriers, few elements a thread save
-// registers.  Measured on a B200, forward + backward pairs replayed in a graph:
-// backward 8192 x 768 bf16 12.3 us with 32 x 24 against 15.5 with 128 x 8;
-// 1000 x 1337 fp32 9.8 us with 256 x 8 against 11.5 with 128 x 16; forward
-// 8191 x 1001 bf16 13.8 us with 64 x 16 against 14.7 with 32 x 32.
+// registers.  Measured on a B200, calls replayed in a graph: backward 8192 x 768
+// bf16 12.3 us with 32 x 24 against 15.5 with 128 x 8; forward 8191 x 1001 bf16
+// 13.8 us with 64 x 16 against 14.7 with 32 x 32.
 struct NormShape {
     int tpr, ept;
 };
@@ -630,11 +627,31 @@ NormShape norm_shape(int d, int vec) {
     if (need <= 512) return {32, 16};
     if (need <= 768) return {32, 24};
     if (need <= 1024) return {64, 16};
-    if (need <= 2048) return {256, 8};
+    if (need <= 2048) return {128, 16};
     if (need <= 4096) return {256, 16};
     if (need <= 8192) return {512, 16};
     if (need <= 16384) return {512, 32};
     return {0, 0};
+}
+
+// The forward's shape: many bf16 rows take 32 elements a thread (16384 x 4096
+// without a residual 45 against 58 us); few rows do not (64 x 4096 3.9 against
+// 3.3 us), nor fp32 rows (8192 x 4096 44.3 against 42.5 us).
+NormShape fwd_shape(int64_t N, int d, int vec) {
+    NormShape f = norm_shape(d, vec);
+    if (vec == 8 && N >= 8 * 148 && f.ept == 16 && f.tpr >= 128) f = {f.tpr / 2, 32};
+    return f;
+}
+
+// The backward's shape.  Rows of 1025 to 2048 elements that start inside a vector
+// would spill registers with 16 elements a thread (1000 x 1337 fp32 11.5 us; 9.8
+// with 256 x 8), whole ones do not (32768 x 2048 bf16 83 us; 98 with 256 x 8).
+// fp32 rows past 8192 elements would need 288 KB of shared memory for one row and
+// the column sums, so they go to the kernels for any width.
+NormShape bwd_shape(int d, int vec) {
+    const NormShape f = norm_shape(d, vec);
+    if (f.tpr == 128 && d % vec != 0) return {256, 8};
+    return f.ept > 24 && vec == 4 ? NormShape{0, 0} : f;
 }
 
 int64_t row_period(int d, int vec) {
@@ -660,13 +677,6 @@ int64_t norm_blocks(int64_t N, int d, int vec, int rpb, int per_sm, int min_rows
 
 constexpr int kBwdMinRows = 2;
 
-// The backward's shape: fp32 rows past 8192 elements would need 288 KB of shared
-// memory for one row and the column sums, so they go to the kernels for any width.
-NormShape bwd_shape(int d, int vec) {
-    const NormShape f = norm_shape(d, vec);
-    return f.tpr == 512 && f.ept > 16 && vec == 4 ? NormShape{0, 0} : f;
-}
-
 // f(tag of TPR, tag of CH, tag of AL) for the shape.
 template <int V> struct Int {
     static constexpr int value = V;
@@ -680,7 +690,9 @@ cudaError_t norm_pick(NormShape n, bool al, F f) {
     };
     if (n.tpr == 32 && n.ept <= 16) return n.ept == 8 ? with(Int<32>{}, Int<8>{}) : with(Int<32>{}, Int<16>{});
     if (n.tpr == 32) return with(Int<32>{}, Int<24>{});
-    if (n.tpr == 64) return with(Int<64>{}, Int<16>{});
+    if (n.tpr == 64) return n.ept == 16 ? with(Int<64>{}, Int<16>{}) : with(Int<64>{}, Int<32>{});
+    if (n.tpr == 128) return n.ept == 16 ? with(Int<128>{}, Int<16>{}) : with(Int<128>{}, Int<32>{});
+    if (n.tpr == 256 && n.ept == 32) return with(Int<256>{}, Int<32>{});
     if (n.tpr == 256) return n.ept == 8 ? with(Int<256>{}, Int<8>{}) : with(Int<256>{}, Int<16>{});
     return n.ept == 16 ? with(Int<512>{}, Int<16>{}) : with(Int<512>{}, Int<32>{});
 }
@@ -718,7 +730,7 @@ cudaError_t launch_norm(const void *x, const void *residual, int dt, const float
     auto go = [&](auto tag) {
         using T = decltype(tag);
         constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-        const NormShape f = norm_shape(d, VEC);
+        const NormShape f = fwd_shape(N, d, VEC);
         if (f.tpr == 0) {
             const int64_t cap = static_cast<int64_t>(kNormSms) * 8;
             return launch_pdl(norm_rows_kernel<T>, dim3(static_cast<unsigned>(N < cap ? N : cap)), dim3(kRowThreads), 0,
@@ -728,16 +740,24 @@ cudaError_t launch_norm(const void *x, const void *residual, int dt, const float
         return norm_pick<T>(f, d % VEC == 0, [&](auto tpr, auto ch, auto al) {
             constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
             using Cfg = NormCfg<TPR, CH * VEC>;
-            constexpr int GROUPS = Cfg::FWD_THREADS / TPR;
-            const int64_t blocks = norm_blocks(N, d, VEC, GROUPS, Cfg::FWD_PER_SM, 1);
-            const size_t smem = static_cast<size_t>(fwd_depth<TPR, CH * VEC>(CH)) * (residual != nullptr ? 2 : 1) * CH *
-                                Cfg::FWD_THREADS * 16;
-            auto kern = norm_fwd_kernel<T, TPR, CH, decltype(al)::value != 0>;
-            cudaError_t e = allow_smem(kern, smem);
-            if (e != cudaSuccess) return e;
-            return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(Cfg::FWD_THREADS), smem, s,
-                              static_cast<const T *>(x), static_cast<const T *>(residual), gamma, beta, eps, N, d,
-                              blocks * GROUPS, static_cast<T *>(y), static_cast<T *>(sum_out), mean, rstd);
+            constexpr int GROUPS = Cfg::THREADS / TPR;
+            if constexpr (CH * VEC == 32 && TPR < 512 && VEC == 4) {
+                return cudaErrorInvalidValue;  // fwd_shape never picks it
+            } else {
+                const int64_t blocks = norm_blocks(N, d, VEC, GROUPS, Cfg::FWD_PER_SM, 1);
+                auto with = [&](auto add) {
+                    constexpr bool ADD = decltype(add)::value != 0;
+                    constexpr size_t smem =
+                        static_cast<size_t>(fwd_depth<TPR, CH * VEC>(ADD ? 2 : 1, CH)) * (ADD ? 2 : 1) * CH * Cfg::THREADS * 16;
+                    auto kern = norm_fwd_kernel<T, TPR, CH, decltype(al)::value != 0, ADD>;
+                    cudaError_t e = allow_smem(kern, smem);
+                    if (e != cudaSuccess) return e;
+                    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(Cfg::THREADS), smem, s,
+                                      static_cast<const T *>(x), static_cast<const T *>(residual), gamma, beta, eps, N, d,
+                                      blocks * GROUPS, static_cast<T *>(y), static_cast<T *>(sum_out), mean, rstd);
+                };
+                return residual != nullptr ? with(Int<1>{}) : with(Int<0>{});
+            }
         });
     };
     return dt == 1 ? go(__nv_bfloat16{}) : go(float{});
@@ -777,22 +797,27 @@ cudaError_t launch_norm_bwd(const void *dy, const void *h, int dt, const float *
         return norm_pick<T>(f, d % VEC == 0, [&](auto tpr, auto ch, auto al) {
             constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
             using Cfg = NormCfg<TPR, CH * VEC>;
-            if constexpr (VEC == 4 && !Cfg::HOLD) {
+            if constexpr (CH * VEC == 32 && (VEC == 4 || TPR < 512)) {
                 return cudaErrorInvalidValue;  // bwd_shape never picks it
             } else {
-                constexpr int GROUPS = Cfg::BWD_THREADS / TPR;
-                size_t smem = static_cast<size_t>(bwd_depth<TPR, CH * VEC>(CH)) * (dres != nullptr ? 3 : 2) * CH *
-                              Cfg::BWD_THREADS * 16;
-                if (!Cfg::HOLD) smem += 2 * sizeof(float) * static_cast<size_t>(CH * VEC) * Cfg::BWD_THREADS;
-                constexpr size_t sums_smem = sizeof(float) * GROUPS * 2 * CH * VEC * (TPR + 4);
-                if (GROUPS > 1 && smem < sums_smem) smem = sums_smem;
-                auto kern = norm_bwd_kernel<T, TPR, CH, decltype(al)::value != 0>;
-                cudaError_t e = allow_smem(kern, smem);
-                if (e != cudaSuccess) return e;
-                return launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(Cfg::BWD_THREADS), smem, s,
-                                  static_cast<const T *>(dy), static_cast<const T *>(h), gamma, mean, rstd,
-                                  static_cast<const T *>(dres), N, d, rows * GROUPS,
-                                  static_cast<int>(row_period(d, VEC)), static_cast<T *>(dx), part);
+                constexpr int GROUPS = Cfg::THREADS / TPR;
+                auto with = [&](auto add) {
+                    constexpr bool ADD = decltype(add)::value != 0;
+                    constexpr size_t ring = static_cast<size_t>(bwd_depth<TPR, CH * VEC>(ADD ? 3 : 2, CH)) * (ADD ? 3 : 2) *
+                                            CH * Cfg::THREADS * 16;
+                    // the column sums lie behind the ring (!HOLD) or, at the end, over it
+                    constexpr size_t own = Cfg::HOLD ? 0 : 2 * sizeof(float) * CH * VEC * Cfg::THREADS;
+                    constexpr size_t sums = GROUPS > 1 ? sizeof(float) * GROUPS * 2 * CH * VEC * (TPR + 4) : 0;
+                    constexpr size_t smem = ring + own > sums ? ring + own : sums;
+                    auto kern = norm_bwd_kernel<T, TPR, CH, decltype(al)::value != 0, ADD>;
+                    cudaError_t e = allow_smem(kern, smem);
+                    if (e != cudaSuccess) return e;
+                    return launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(Cfg::THREADS), smem, s,
+                                      static_cast<const T *>(dy), static_cast<const T *>(h), gamma, mean, rstd,
+                                      static_cast<const T *>(dres), N, d, rows * GROUPS,
+                                      static_cast<int>(row_period(d, VEC)), static_cast<T *>(dx), part);
+                };
+                return dres != nullptr ? with(Int<1>{}) : with(Int<0>{});
             }
         });
     };
