@@ -374,8 +374,9 @@ MOE_API moe_status moe_backward(const void *x, moe_dtype dt, const float *W_g, c
  *  y            device [N, d] of dt out
  *  sum_out      device [N, d] of dt out: h; required with a residual, else NULL
  *  mean, rstd   device [N] fp32 out, each nullable
- * y or sum_out (not both) may be the array x or residual itself.  Any d >= 1;
- * rows may start at any multiple of the element size. */
+ * y or sum_out (not both) may be the array x or residual itself; no other
+ * overlap.  Any 1 <= d <= 2^30; rows may start at any multiple of the element
+ * size. */
 MOE_API moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, const float *gamma,
                                   const float *beta, float eps, int64_t N, int d, void *y, void *sum_out,
                                   float *mean, float *rstd, void *stream);
@@ -409,8 +410,12 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dt
  *  y         device [N, d_out] of dt out, rounded once
  *  z_out     device [N, d_out] of dt out, nullable: z rounded, for moe_linear_backward
  *  ws        scratch of moe_linear_workspace_size() bytes (NULL if that is 0)
- * fp32 accumulation.  A wait of its kernels that runs out is recorded in the
- * library's own per-device word: moe_check_linear_status(). */
+ * 1 <= d_in, d_out <= 2^30.  No other overlap of outputs and inputs.  fp32
+ * accumulation.  fp32 storage keeps fp32's precision (products of three bf16
+ * parts on the tensor cores, or fp32 on CUDA cores for a few tokens) for finite
+ * values below 3.38e38; an infinite one gives NaN.  A wait of its kernels that
+ * runs out is recorded in the library's own per-device word:
+ * moe_check_linear_status(). */
 MOE_API size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt);
 MOE_API moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b, int activation,
                               const void *residual, int64_t N, int d_in, int d_out, void *y, void *z_out, void *ws,

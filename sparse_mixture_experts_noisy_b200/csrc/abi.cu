@@ -67,10 +67,23 @@ moe_status check_shape(int64_t N, int d, int E, int k, moe_dtype dt) {
     return MOE_OK;
 }
 
+// Rows of the layer norm and of the dense layer: widths whose indices, rounded up
+// to a tile, fit in int.
+constexpr int kMaxWidth = 1 << 30;
+
+moe_status check_norm(int64_t N, int d, moe_dtype dt) {
+    moe_status st = check_shape(N, d, 1, 1, dt);
+    if (st != MOE_OK) return st;
+    if (d > kMaxWidth) return fail(MOE_ERR_INVALID_ARG, "d must be at most 2^30 (got %d)", d);
+    return MOE_OK;
+}
+
 moe_status check_linear(int64_t N, int d_in, int d_out, moe_dtype dt, int activation) {
     moe_status st = check_shape(N, d_in, 1, 1, dt);
     if (st != MOE_OK) return st;
     if (d_out < 1) return fail(MOE_ERR_INVALID_ARG, "d_out must be >= 1 (got %d)", d_out);
+    if (d_in > kMaxWidth || d_out > kMaxWidth)
+        return fail(MOE_ERR_INVALID_ARG, "d_in and d_out must be at most 2^30 (got %d, %d)", d_in, d_out);
     if (activation != MOE_ACT_NONE && activation != MOE_ACT_RELU && activation != MOE_ACT_GELU)
         return fail(MOE_ERR_INVALID_ARG, "activation must be MOE_ACT_NONE, MOE_ACT_RELU or MOE_ACT_GELU");
     return MOE_OK;
@@ -628,7 +641,7 @@ moe_status moe_load_stats(const int32_t *topk_idx, const float *gates, int64_t N
 moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, const float *gamma, const float *beta,
                           float eps, int64_t N, int d, void *y, void *sum_out, float *mean, float *rstd,
                           void *stream) {
-    moe_status st = check_shape(N, d, 1, 1, dt);
+    moe_status st = check_norm(N, d, dt);
     if (st != MOE_OK) return st;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be > 0 and finite (got %g)", eps);
     OPTIONAL_PTR(gamma, "gamma");
@@ -651,14 +664,14 @@ moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, con
 }
 
 size_t moe_layer_norm_backward_workspace_size(int64_t N, int d, moe_dtype dt) {
-    if (check_shape(N, d, 1, 1, dt) != MOE_OK) return 0;
+    if (check_norm(N, d, dt) != MOE_OK) return 0;
     return moe::norm_bwd_ws_bytes(N, d, dt == MOE_BF16 ? 1 : 0);
 }
 
 moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, const float *gamma, const float *mean,
                                    const float *rstd, const void *dres, int64_t N, int d, void *dx, float *dgamma,
                                    float *dbeta, void *ws, size_t ws_bytes, void *stream) {
-    moe_status st = check_shape(N, d, 1, 1, dt);
+    moe_status st = check_norm(N, d, dt);
     if (st != MOE_OK) return st;
     OPTIONAL_PTR(gamma, "gamma");
     OPTIONAL_PTR(dres, "dres");
@@ -683,7 +696,7 @@ moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, 
 }
 
 size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt) {
-    if (check_shape(N, d_in, 1, 1, dt) != MOE_OK || d_out < 1) return 0;
+    if (check_linear(N, d_in, d_out, dt, MOE_ACT_NONE) != MOE_OK) return 0;
     return moe::linear_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0);
 }
 

@@ -883,6 +883,15 @@ ProdArgs prod_args(const TcProduct &t) {
     return ProdArgs{t.M, t.Nn, (t.K + kBK - 1) / kBK, t.p_mn ? 1 : 0, t.q_mn ? 1 : 0, 0, t.epi};
 }
 
+// Limit of a wait: the base, and for the epilogue's wait on a whole tile about ten
+// times what the tile's K blocks take.
+uint64_t wait_limit(uint64_t base, const TcProduct *t, int count, bool fp32) {
+    int kb = 0;
+    for (int i = 0; i < count; ++i)
+        if ((t[i].K + kBK - 1) / kBK > kb) kb = (t[i].K + kBK - 1) / kBK;
+    return base + static_cast<uint64_t>(kb) * (fp32 ? 20000u : 5000u);
+}
+
 // Tensor maps of both operands: `planes` planes of [k][row] or [row][k], each
 // row `ld` elements (a multiple of 8).
 bool operand_map(CUtensorMap *m, const void *base, int planes, int64_t rows, int K, bool mn, int box) {
@@ -997,7 +1006,7 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     }
     a.stages = kPairRing / (PLANES * (128 * kBK * 2 + a.q_room));
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
-    a.timeout_ns = timeout_ns;
+    a.timeout_ns = wait_limit(timeout_ns, t, count, SPLIT);
     return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
 }
 
@@ -1031,7 +1040,7 @@ cudaError_t launch_split(const TcProduct *t, int count, int S, uint64_t timeout_
     a.S = S;
     a.stages = (kSplitSmem / split_ctas(SPLIT) - 1024) / stage_bytes;
     if (a.stages > 6) a.stages = 6;
-    a.timeout_ns = timeout_ns;
+    a.timeout_ns = wait_limit(timeout_ns, t, count, SPLIT);
     const int ring = a.stages * stage_bytes;
     const int smem = 1024 + (ring > BN * 512 ? ring : BN * 512);
     auto kern = linear_split_kernel<T, BN>;

@@ -32,6 +32,7 @@ def test_layer_norm_arguments(L):
                 dict(eps=float("inf")), dict(x=None), dict(y=None), dict(x=ODD), dict(gamma=ODD), dict(beta=ODD),
                 dict(mean=ODD), dict(rstd=ODD), dict(res=ODD, s=A), dict(N=1 << 31)):
         assert call(**bad) == 1, bad
+    assert call(d=(1 << 30) + 1, N=1) == 1 and "2^30" in _err(L)
     assert call(res=A) == 1 and "sum_out" in _err(L)
     assert call(s=A) == 1 and "sum_out must be NULL" in _err(L)
     assert call(res=A, s=B) == 1 and "different arrays" in _err(L)
@@ -65,6 +66,9 @@ def test_linear_arguments(L):
                 dict(res=ODD), dict(ws=ODD)):
         assert call(**bad) == 1, bad
     assert call(z=B) == 1 and "different arrays" in _err(L)
+    for wide in (dict(d_in=(1 << 30) + 1), dict(d_out=(1 << 30) + 1)):
+        assert call(N=1, **wide) == 1 and "2^30" in _err(L)
+        assert L.moe_linear_workspace_size(1, wide.get("d_in", 8), wide.get("d_out", 8), 0) == 0
     if need:
         assert call(ws=None) == 3 and call(n=need - 1) == 3
     assert call(N=0, x=None, y=None) == 0
