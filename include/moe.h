@@ -13,6 +13,8 @@
  *       second choices, tokens in order; places >= C dropped)
  *     E_e(x) = W_down[e] ReLU(W_up[e] x)         expert FFN
  *     y     = sum over kept choices of g * E_e(x)
+ * Around it: layer norm with the residual add, and a dense layer with bias,
+ * activation and residual, each with its backward pass.
  *
  * Conventions shared by every call
  * --------------------------------
