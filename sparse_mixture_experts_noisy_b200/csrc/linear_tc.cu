@@ -244,13 +244,19 @@ __device__ __forceinline__ void store_cols(const LinearEpi &e, const float *acc,
 // of which an epilogue thread adds 96 columns in registers.
 // Persistent, one pair per two SMs; two accumulators, so the epilogue of
 // one tile (or piece) overlaps the MMAs of the next.  Warp 0: TMA; warp 1: MMA;
-// warps 2-9: epilogue, two groups of four, each half of the m.
+// the others: epilogue, in groups of four, each a share of the m.
 //
 // One launch runs one product or two (dW, then dx).  A unit is a tile of a
 // product; the first product's units are dealt in turn, and the second's start
 // with the pairs that got one fewer of the first's, as many as fit into the time
 // the others still need, before they are dealt to all.
-constexpr int kPairThreads = 320;
+// Epilogue warps come in groups of four, which read all 128 lanes of tensor
+// memory; two groups share a tile's rows.  bf16 tiles have two such sets, one for
+// each accumulator: a set spends most of a short tile's epilogue on its own chain
+// of waits, reads and stores, and the other works meanwhile.  An fp32 thread's
+// sums need the registers of one set.
+constexpr int pair_groups(bool fp32) { return fp32 ? 2 : 4; }
+constexpr int pair_threads(bool fp32) { return 64 + 128 * pair_groups(fp32); }
 constexpr int kPairMaxStages = 6;
 constexpr int kPairRing = 216 * 1024;
 constexpr int pair_max_tm(bool fp32) { return fp32 ? 192 : 256; }
@@ -293,20 +299,21 @@ __device__ __forceinline__ bool pair_unit(const PairArgs &a, int pair, int npair
     const int mt = static_cast<int>((p.M + p.tm - 1) / p.tm), nt = (p.Nn + 255) / 256;
     const int sweep = kGroupM * nt;
     const int grp = u / sweep, rem = u - grp * sweep;
-    const int rows = mt - grp * kGroupM < kGroupM ? mt - grp * kGroupM : kGroupM;
-    t.m0 = static_cast<int64_t>(grp * kGroupM + rem % rows) * p.tm;
-    t.n0 = rem / rows * 256;
+    const int rows = mt - grp * kGroupM;  // m tiles of the last group
+    const int row = rows < kGroupM ? rem % rows : rem % kGroupM, col = rows < kGroupM ? rem / rows : rem / kGroupM;
+    t.m0 = static_cast<int64_t>(grp * kGroupM + row) * p.tm;
+    t.n0 = col * 256;
     return true;
 }
 
 template <typename T, bool FULL>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(sizeof(T) == 4), 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constant__ CUtensorMap tq0,
                    const __grid_constant__ CUtensorMap tp1, const __grid_constant__ CUtensorMap tq1,
                    const __grid_constant__ PairArgs args) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
-    constexpr int HMAX = pair_max_tm(SPLIT) / 2;
+    constexpr int SETS = pair_groups(SPLIT) / 2, HMAX = pair_max_tm(SPLIT) / 2;
     constexpr uint32_t P_BYTES = 128 * kBK * 2, Q_AT = PLANES * P_BYTES;
     const int stages = args.stages;
     const uint32_t q_room = args.q_room, stage_bytes = PLANES * (P_BYTES + q_room);
@@ -337,7 +344,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
         }
         mbar_init(tfull0, 1);
         mbar_init(tfull0 + 8, 1);
-        mbar_init(tempty0, 16);  // 8 epilogue warps in each CTA
+        mbar_init(tempty0, 16);  // a set's 8 epilogue warps in each CTA
         mbar_init(tempty0 + 8, 16);
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -487,11 +494,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
             }
         }
     } else {
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        int local = 0;
+        const int q = warp & 3, half = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3;
+        int local = set;  // pieces before this one, over all sets: the accumulators' turn
         bool ok = true;
         PairUnit t;
-        for (int i = 0; ok && pair_unit(args, pair, npairs, n1, i, t); ++i) {
+        for (int i = set; ok && pair_unit(args, pair, npairs, n1, i, t); i += SETS) {
             const ProdArgs &p = args.p[t.prob];
             const int n = t.n0 + static_cast<int>(rank) * 128 + q * 32 + lane;
             const int hm = p.tm / 2;  // m of this group
@@ -559,7 +566,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
                     if (leader) mbar_arrive(tempty0 + 8 * acc);
                     else mbar_arrive_cluster(tempty0_lead + 8 * acc);
                 }
-                ++local;
+                local += SETS;
             }
             if constexpr (SPLIT) {
                 if (ok && n < p.Nn) {
@@ -973,7 +980,7 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
         pairs = num_sms / 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * pairs);
-        cfg.blockDim = dim3(kPairThreads);
+        cfg.blockDim = dim3(pair_threads(SPLIT));
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
         int max_clusters = 0;
@@ -1007,7 +1014,7 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     a.stages = kPairRing / (PLANES * (128 * kBK * 2 + a.q_room));
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     a.timeout_ns = wait_limit(timeout_ns, t, count, SPLIT);
-    return launch_pdl(kern, dim3(2 * pairs), dim3(kPairThreads), smem, s, mp[0], mq[0], mp[1], mq[1], a);
+    return launch_pdl(kern, dim3(2 * pairs), dim3(pair_threads(SPLIT)), smem, s, mp[0], mq[0], mp[1], mq[1], a);
 }
 
 int64_t split_tiles(const TcProduct &t, int bn) {
