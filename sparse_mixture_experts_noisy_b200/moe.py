@@ -511,7 +511,7 @@ def moe_linear(x, W, b=None, act=ACT_NONE, residual=None, keep_z=False, y=None, 
     the pre-activations, for moe_linear_backward).  x [N, d_in] and W [d_out,
     d_in] of one dtype, b [d_out] fp32; residual may be y itself."""
     N, d_in = _matrix(x, "x")
-    d_out = _matrix(W, "W")[0]
+    d_out = W.shape[0]
     if (at := _elsewhere(x, stream)) is not None:
         with at:
             return moe_linear(x, W, b, act, residual, keep_z, y, ws)
@@ -537,7 +537,7 @@ def moe_linear_backward(dy, x, W, act=ACT_NONE, z=None, want_dx=True, want_dW=Tr
     pre-activations (keep_z), needed unless act is ACT_NONE.
     -> dict(dx [N, d_in] of x's dtype, dW [d_out, d_in] of W's dtype, db [d_out] fp32; None where not wanted)."""
     N, d_in = _matrix(x, "x")
-    d_out = _matrix(W, "W")[0]
+    d_out = W.shape[0]
     if (at := _elsewhere(x, stream)) is not None:
         with at:
             return moe_linear_backward(dy, x, W, act, z, want_dx, want_dW, want_db, ws)
