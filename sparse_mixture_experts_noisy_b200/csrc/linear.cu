@@ -218,8 +218,14 @@ cudaError_t pack(const void *&in0, int64_t rows0, void *out0, const void *&in1, 
 
 // A few tokens: the CUDA-core kernels, unless W is an operand as it is, which
 // streams as fast through the tensor cores.  For fp32 they save a copy of W in
-// parts, 2.5 times its bytes.
-bool use_skinny(int64_t M, int dt, int cols) { return M <= kSkinnyRows && needs_pack(dt, cols); }
+// parts, 2.5 times its bytes: 16 x 4096 -> 4096 32 us, 45 through the tensor
+// cores.  Padding a bf16 W costs less: 16 x 2281 -> 8176 39 and 23 us, 4 tokens 15
+// and 22; while W is small the saved launch counts more (16 x 301 -> 705 3.8 and
+// 7.0 us).
+bool use_skinny(int64_t M, int dt, int cols, int other) {
+    if (!needs_pack(dt, cols) || M > kSkinnyRows) return false;
+    return dt == 0 || M <= 4 || static_cast<int64_t>(cols) * other <= (1 << 20);
+}
 // dW has no weights to copy, and its CUDA-core kernel is bound by arithmetic past
 // a few tokens: bf16 9200 x 11200 from 6 tokens 76 us, from 16 at 4096 x 14336
 // 121 us, where the tensor cores take about 35: kSkinnyDwRows.
@@ -229,7 +235,7 @@ struct FwdScratch {
 };
 FwdScratch fwd_scratch(int64_t M, int d_in, int d_out, int dt) {
     FwdScratch L{};
-    if (M == 0 || !needs_pack(dt, d_in) || use_skinny(M, dt, d_in)) return L;
+    if (M == 0 || !needs_pack(dt, d_in) || use_skinny(M, dt, d_in, d_out)) return L;
     L.W = operand_bytes(M, d_in, dt);
     L.total = L.W + operand_bytes(d_out, d_in, dt);
     return L;
@@ -245,7 +251,10 @@ struct BwdWays {
 BwdWays bwd_ways(int64_t M, int d_in, int d_out, int dt, int act) {
     BwdWays w{};
     w.dw_skinny = M <= kSkinnyDwRows;
-    w.dx_skinny = use_skinny(M, dt, d_in) || use_skinny(M, dt, d_out);
+    // few columns and a long sum leave that kernel a few CTAs with many rows each
+    // (backward of 9 x 272 -> 5696 fp32 45 us; 27 with dx on the tensor cores)
+    const int vec = dt == 1 ? 8 : 4, tiles = (d_in - 1) / (d_in % vec == 0 ? 32 * vec : 32) + 1;
+    w.dx_skinny = (use_skinny(M, dt, d_in, d_out) || use_skinny(M, dt, d_out, d_in)) && (tiles >= 16 || d_out <= 4096);
     const bool tc = !w.dw_skinny || !w.dx_skinny, same = !needs_pack(dt, d_out);
     w.operand = tc && (act != kActNone || !same);
     w.plain = (w.dw_skinny || w.dx_skinny) && act != kActNone && !(w.operand && same);
@@ -284,7 +293,7 @@ cudaError_t launch_linear(const LinearArgs &a, void *ws, uint64_t timeout_ns, in
     const LinearEpi epi{a.b, a.act, a.residual, a.y, a.z_out};
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        if (use_skinny(a.M, a.dt, a.d_in))
+        if (use_skinny(a.M, a.dt, a.d_in, a.d_out))
             return launch_skinny_fwd<T>(static_cast<const T *>(a.x), static_cast<const T *>(a.W), a.M, a.d_in, a.d_out,
                                         epi, s);
         const void *x = a.x, *W = a.W;

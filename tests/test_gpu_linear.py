@@ -278,3 +278,14 @@ def test_offsets_past_32_bits():
     y = moe.moe_linear(x, W, act=moe.ACT_RELU)
     want = (x[-200:].double() @ W.double().t()).clamp(min=0)
     close(y[-200:], want, 2 ** -8 * want.abs() + 68 * 2 * U * (x[-200:].double().abs() @ W.double().abs().t()), "y")
+
+
+def test_few_tokens_of_wide_rows():
+    """Around the token counts and weight sizes where another kernel takes over."""
+    require_gpu()
+    for n in (1, 4, 5, 8, 9, 16, 17):
+        for d_in, d_out in ((1001, 1337), (1031, 1033), (2048, 1029), (1027, 1032)):
+            for dtype in (torch.bfloat16, torch.float32):
+                t = make(n, d_in, d_out, dtype, seed=n)
+                _, z = check_forward(t, "gelu")
+                check_backward(t, z, "gelu")
