@@ -1,7 +1,8 @@
-// The dense layer's products for a few tokens (M <= 16), on CUDA cores: each
-// weight is read once (or written once, for dW) with 16-byte accesses and meets
-// all M tokens in registers, so the kernels run at the rate of W's bytes and
-// need no copy of W in another form.  fp32 accumulation in fp32 storage too.
+// The dense layer's products for a few tokens, on CUDA cores: each weight is read
+// once (or written once, for dW) with 16-byte accesses and meets up to 16 tokens
+// in registers, so the kernels run at the rate of W's bytes and need no copy of W
+// in another form.  The forward takes more tokens of a small W in further blocks, 16
+// each.  fp32 accumulation in fp32 storage too.
 //   forward  z[m][n]  = sum_k x[m][k] W[n][k]       rows of W, K split over a block's warps
 //   dx       dx[m][i] = sum_o dZ[m][o] W[o][i]      columns of W, o split over warps and a cluster
 //   dW       dW[o][i] = sum_m dZ[m][o] x[m][i]      one pass over dW
@@ -74,6 +75,9 @@ __device__ __forceinline__ void fold(float *v, int lane) {
 template <typename T, int VEC, int MT, int R, int KW>
 __global__ void __launch_bounds__(kThreads)
 skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K, int Nn, const LinearEpi epi) {
+    const int m0 = blockIdx.y * MT;  // this block's tokens
+    x += static_cast<int64_t>(m0) * K;
+    M -= m0;
     constexpr int V = R * MT, GROUPS = kWarps / KW;
     static_assert(V % 32 == 0 || (V < 32 && (V & (V - 1)) == 0), "fold");
     __shared__ float red[kWarps][V];
@@ -117,7 +121,7 @@ skinny_fwd_kernel(const T *__restrict__ x, const T *__restrict__ W, int M, int K
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) sum += red[g * KW + w][v];
-            linear_store<T>(epi, m, n, Nn, sum);
+            linear_store<T>(epi, m0 + m, n, Nn, sum);
         }
     }
 }
@@ -284,8 +288,9 @@ cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, 
         constexpr int V = decltype(vec)::value, MT = decltype(mt)::value;
         auto go = [&](auto r, auto kw) {
             constexpr int R = decltype(r)::value, KW = decltype(kw)::value, rows = R * (kWarps / KW);
-            return launch_pdl(skinny_fwd_kernel<T, V, MT, R, KW>, dim3(static_cast<unsigned>((Nn + rows - 1) / rows)),
-                              dim3(kThreads), 0, s, x, W, static_cast<int>(M), K, Nn, epi);
+            const dim3 grid(static_cast<unsigned>((Nn + rows - 1) / rows), static_cast<unsigned>((M + MT - 1) / MT));
+            return launch_pdl(skinny_fwd_kernel<T, V, MT, R, KW>, grid, dim3(kThreads), 0, s, x, W,
+                              static_cast<int>(M), K, Nn, epi);
         };
         constexpr int R = MT > 1 ? 4 : 2;
         return K >= 8 * 32 * V || Nn < 148 * kWarps ? go(Int<R>{}, Int<kWarps>{}) : go(Int<R>{}, Int<1>{});

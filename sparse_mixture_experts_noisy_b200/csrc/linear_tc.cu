@@ -1117,9 +1117,13 @@ cudaError_t run_split(const TcProduct *t, int count, uint64_t timeout_ns, int nu
 
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s) {
-    // products of one kind share a launch
+    // products of one kind share a launch; on the split kernel only if their K are
+    // alike, since they share the number of splits (backward of 11 x 192 -> 4432 fp32
+    // 48 us in one launch, 27 in two)
     const bool first = use_pairs(t[0], fp32, num_sms);
-    if (count == 2 && use_pairs(t[1], fp32, num_sms) != first) {
+    const bool alike = count == 1 || first || (t[0].K <= 4 * static_cast<int64_t>(t[1].K) + 512 &&
+                                               t[1].K <= 4 * static_cast<int64_t>(t[0].K) + 512);
+    if (count == 2 && (use_pairs(t[1], fp32, num_sms) != first || !alike)) {
         cudaError_t e = launch_tc_products(t, 1, fp32, full, timeout_ns, num_sms, s);
         return e != cudaSuccess ? e : launch_tc_products(t + 1, 1, fp32, full, timeout_ns, num_sms, s);
     }

@@ -28,9 +28,9 @@ struct TcProduct {
 cudaError_t launch_tc_products(const TcProduct *t, int count, bool fp32, bool full, uint64_t timeout_ns, int num_sms,
                                cudaStream_t s);
 
-// M <= kSkinnyRows or kSkinnyDwRows tokens; rows dense, of any width.  dz: dZ in the storage type.
-constexpr int kSkinnyRows = 16;   // forward and dx
-constexpr int kSkinnyDwRows = 4;  // dW
+// For a few tokens; rows dense, of any width.  dz: dZ in the storage type.
+constexpr int kSkinnyRows = 16;   // dx at most; forward: a block's
+constexpr int kSkinnyDwRows = 4;  // dW at most
 template <typename T>
 cudaError_t launch_skinny_fwd(const T *x, const T *W, int64_t M, int K, int Nn, const LinearEpi &epi, cudaStream_t s);
 template <typename T>

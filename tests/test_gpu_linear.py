@@ -283,8 +283,9 @@ def test_offsets_past_32_bits():
 def test_few_tokens_of_wide_rows():
     """Around the token counts and weight sizes where another kernel takes over."""
     require_gpu()
-    for n in (1, 4, 5, 8, 9, 16, 17):
-        for d_in, d_out in ((1001, 1337), (1031, 1033), (2048, 1029), (1027, 1032)):
+    for n in (1, 4, 5, 8, 9, 16, 17, 33, 64, 65):
+        for d_in, d_out in ((1001, 1337), (1031, 1033), (2048, 1029), (1027, 1032), (300, 700), (140, 2000),
+                            (192, 4432)):
             for dtype in (torch.bfloat16, torch.float32):
                 t = make(n, d_in, d_out, dtype, seed=n)
                 _, z = check_forward(t, "gelu")
