@@ -712,6 +712,8 @@ moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b
         REQUIRE_PTR(x, "x");
         REQUIRE_PTR(y, "y");
         if (z_out == y) return fail(MOE_ERR_INVALID_ARG, "y and z_out must be different arrays");
+        if (y == x || y == W || (z_out != nullptr && (z_out == x || z_out == W || z_out == residual)))
+            return fail(MOE_ERR_INVALID_ARG, "an output must not be an input (residual may be y)");
     }
     const size_t need = moe::linear_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0);
     if (need > 0 && (ws == nullptr || ws_bytes < need))
@@ -743,6 +745,9 @@ moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, cons
         REQUIRE_PTR(dy, "dy");
         REQUIRE_PTR(x, "x");
         if (activation != MOE_ACT_NONE) REQUIRE_PTR(z, "z");
+        for (const void *out : {static_cast<const void *>(dx), static_cast<const void *>(dW)})
+            if (out != nullptr && (out == dy || out == x || out == W || out == z))
+                return fail(MOE_ERR_INVALID_ARG, "dx and dW must not be an input");
     }
     const size_t need = moe::linear_bwd_ws_bytes(N, d_in, d_out, dt == MOE_BF16 ? 1 : 0, activation);
     if (need > 0 && (ws == nullptr || ws_bytes < need))

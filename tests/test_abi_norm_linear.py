@@ -90,6 +90,16 @@ def test_linear_backward_arguments(L):
     assert L.moe_linear_backward_workspace_size(100, 64, 48, 9, 0) == 0
 
 
+def test_linear_outputs_are_not_inputs(L):
+    X, W, Z = 0x500000, 0x600000, 0x700000
+    for y, z in ((X, None), (W, None), (B, X), (B, W), (B, Z)):
+        assert L.moe_linear(X, 1, W, None, 0, Z, 4, 64, 64, y, z, None, 0, None) == 1 and "input" in _err(L)
+    for out in (A, X, W, Z):
+        for dx, dW in ((out, None), (None, out)):
+            assert L.moe_linear_backward(A, X, 1, W, Z, 2, 4, 64, 64, dx, dW, None, A, BIG, None) == 1
+            assert "must not be an input" in _err(L)
+
+
 def test_binding_refuses_what_it_cannot_pass(L):
     x, W = torch.zeros(4, 8), torch.zeros(6, 8)
     for f in (lambda: moe.moe_layer_norm(x), lambda: moe.moe_linear(x, W),
