@@ -89,6 +89,16 @@ moe_status check_linear(int64_t N, int d_in, int d_out, moe_dtype dt, int activa
     return MOE_OK;
 }
 
+// SMs of the current device for the dense layer's launch plans, which divide by
+// the CTA pairs that it holds.  MOE_ERR_CUDA where the device cannot be asked.
+moe_status linear_sms(int &sms) {
+    sms = num_sms_current();
+    if (sms >= 2) return MOE_OK;
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? cuda_fail(e, "device query")
+                            : fail(MOE_ERR_CUDA, "device query: the dense layer needs a device of two SMs (got %d)", sms);
+}
+
 #define REQUIRE_PTR(p, name)                                                                    \
     do {                                                                                        \
         if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s must not be NULL", name);      \
@@ -720,8 +730,11 @@ moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b
         return fail(MOE_ERR_WORKSPACE, "linear workspace needs %zu bytes (got %zu)", need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     OPTIONAL_PTR(ws, "ws");
+    if (N == 0) return MOE_OK;
+    int sms = 0;
+    if ((st = linear_sms(sms)) != MOE_OK) return st;
     moe::LinearArgs a{x, dt == MOE_BF16 ? 1 : 0, W, b, activation, residual, N, d_in, d_out, y, z_out};
-    cudaError_t e = moe::launch_linear(a, ws, kWaitTimeoutNs, num_sms_current(), static_cast<cudaStream_t>(stream));
+    cudaError_t e = moe::launch_linear(a, ws, kWaitTimeoutNs, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "linear launch");
     return MOE_OK;
 }
@@ -754,8 +767,10 @@ moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, cons
         return fail(MOE_ERR_WORKSPACE, "linear backward workspace needs %zu bytes (got %zu)", need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     OPTIONAL_PTR(ws, "ws");
+    int sms = 0;
+    if ((st = linear_sms(sms)) != MOE_OK) return st;
     moe::LinearBwdArgs a{dy, x, dt == MOE_BF16 ? 1 : 0, W, z, activation, N, d_in, d_out, dx, dW, db};
-    cudaError_t e = moe::launch_linear_bwd(a, ws, kWaitTimeoutNs, num_sms_current(), static_cast<cudaStream_t>(stream));
+    cudaError_t e = moe::launch_linear_bwd(a, ws, kWaitTimeoutNs, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "linear backward launch");
     return MOE_OK;
 }
