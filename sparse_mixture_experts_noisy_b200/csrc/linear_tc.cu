@@ -601,6 +601,26 @@ constexpr int split_ctas(bool fp32) { return fp32 ? 1 : 2; }
 constexpr int kSplitSmem = 216 * 1024;
 
 template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
+template <typename T, int BN> constexpr int split_stage_bytes(bool mn) {
+    return (sizeof(T) == 4 ? 3 : 1) * (128 * kBK * 2 + split_b_bytes<BN>(mn));
+}
+// Stages of a ring, and a launch's shared memory: the ring, over which the sums go.
+constexpr int kSplitMaxStages = 6;
+constexpr int split_stages(bool fp32, int stage_bytes) {
+    const int n = (kSplitSmem / split_ctas(fp32) - 1024) / stage_bytes;
+    return n > kSplitMaxStages ? kSplitMaxStages : n;
+}
+template <typename T, int BN> constexpr int split_smem(int stage_bytes) {
+    const int ring = split_stages(sizeof(T) == 4, stage_bytes) * stage_bytes;
+    return 1024 + (ring > BN * 512 ? ring : BN * 512);
+}
+// The most that any launch of the kernel asks for.  The limit set on a kernel is
+// this one whatever the call needs: it belongs to the kernel, and a call that set
+// a smaller one would take it from under another thread's launch.
+template <typename T, int BN> constexpr int split_smem_limit() {
+    const int k = split_smem<T, BN>(split_stage_bytes<T, BN>(false)), mn = split_smem<T, BN>(split_stage_bytes<T, BN>(true));
+    return k > mn ? k : mn;
+}
 
 // One product or two (dW and dx, which share a launch); blocks [0, tiles0 S) are
 // the first's.
@@ -653,7 +673,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_consta
     constexpr int COLS = BN < 32 ? 32 : BN;  // tensor-memory columns of one accumulator
     constexpr uint32_t TMEM_COLS = 2 * COLS;
     constexpr uint32_t A_BYTES = 128 * kBK * 2;
-    constexpr int kMaxStages = 6;
+    constexpr int kMaxStages = kSplitMaxStages;
     const int S = args.S, stages = args.stages;
     const uint64_t tmo = args.timeout_ns;
     int tile = static_cast<int>(blockIdx.x / static_cast<unsigned>(S));
@@ -1034,7 +1054,7 @@ cudaError_t launch_split(const TcProduct *t, int count, int S, uint64_t timeout_
             !operand_map(&mq[i], t[i].Q, PLANES, t[i].M, t[i].K, t[i].q_mn, BN))
             return cudaErrorInvalidValue;
         a.p[i] = prod_args(t[i]);
-        const int b = PLANES * (128 * kBK * 2 + split_b_bytes<BN>(t[i].q_mn));
+        const int b = split_stage_bytes<T, BN>(t[i].q_mn);
         if (b > stage_bytes) stage_bytes = b;
         tiles += split_tiles(t[i], BN);
         if (i == 0) a.tiles0 = static_cast<int>(tiles);
@@ -1045,13 +1065,11 @@ cudaError_t launch_split(const TcProduct *t, int count, int S, uint64_t timeout_
     }
     if (tiles * S > INT32_MAX) return cudaErrorInvalidValue;
     a.S = S;
-    a.stages = (kSplitSmem / split_ctas(SPLIT) - 1024) / stage_bytes;
-    if (a.stages > 6) a.stages = 6;
+    a.stages = split_stages(SPLIT, stage_bytes);
     a.timeout_ns = wait_limit(timeout_ns, t, count, SPLIT);
-    const int ring = a.stages * stage_bytes;
-    const int smem = 1024 + (ring > BN * 512 ? ring : BN * 512);
+    const int smem = split_smem<T, BN>(stage_bytes);
     auto kern = linear_split_kernel<T, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem_limit<T, BN>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
