@@ -60,7 +60,8 @@ moe_status check_shape(int64_t N, int d, int E, int k, moe_dtype dt) {
     if (dt != MOE_F32 && dt != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype must be MOE_F32 or MOE_BF16");
     if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
     if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d must be >= 1 (got %d)", d);
-    if (E < 1 || E > 256) return fail(MOE_ERR_INVALID_ARG, "E must be in [1, 256] (got %d)", E);
+    if (E < 1 || E > moe::kMaxExperts)
+        return fail(MOE_ERR_INVALID_ARG, "E must be in [1, %d] (got %d)", moe::kMaxExperts, E);
     if (k < 1 || k > E) return fail(MOE_ERR_INVALID_ARG, "k must be in [1, E] (got k=%d, E=%d)", k, E);
     if (N * static_cast<int64_t>(k) > INT32_MAX)
         return fail(MOE_ERR_INVALID_ARG, "N * k must fit in int32 (got %lld)", (long long)(N * k));

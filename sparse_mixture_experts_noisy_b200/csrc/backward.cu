@@ -341,7 +341,9 @@ cudaError_t launch_tail(const BwdArgs &a, const void *dX, float *ds, float *part
     const size_t smem = sizeof(float) * static_cast<size_t>(a.E) * 128;
     auto kern = bwd_router_part_kernel<T>;
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // the largest of any call, so that no thread lowers another's limit
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(sizeof(float) * kMaxExperts * 128));
         if (e != cudaSuccess) return e;
     }
     e = launch_pdl(kern, dim3(P, cblocks), dim3(128), smem, s, static_cast<const T *>(a.x),

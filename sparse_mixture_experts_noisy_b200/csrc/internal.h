@@ -7,6 +7,8 @@
 
 namespace moe {
 
+constexpr int kMaxExperts = 256;
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Launch with programmatic dependent launch allowed: the kernel may be

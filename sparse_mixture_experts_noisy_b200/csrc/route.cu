@@ -342,6 +342,11 @@ route_block_kernel(const T *__restrict__ x, const float *__restrict__ W_g,
     }
 }
 
+constexpr size_t route_tile_smem(int E, int k) {
+    return sizeof(float) * (static_cast<size_t>(kTileEC) * kTileDC + static_cast<size_t>(kTileTok) * E +
+                            static_cast<size_t>(kTileWarps) * 2 * k);
+}
+
 template <typename T, int VEC>
 cudaError_t launch_route_v(const void *x, const float *W_g, const float *b_g, const float *noise,
                            float sigma, int64_t N, int d, int E, int k, float *logits_out,
@@ -353,11 +358,13 @@ cudaError_t launch_route_v(const void *x, const float *W_g, const float *b_g, co
                           b_g, noise, sigma, N, d, E, k, logits_out, topk_idx, gates, status);
     }
     const int64_t blocks = (N + kTileTok - 1) / kTileTok;
-    const size_t smem = sizeof(float) * (static_cast<size_t>(kTileEC) * kTileDC +
-                                         static_cast<size_t>(kTileTok) * E + static_cast<size_t>(kTileWarps) * 2 * k);
+    const size_t smem = route_tile_smem(E, k);
     auto kern = route_tile_kernel<T, VEC>;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // the largest of any call: a limit by this call's need would be taken from
+        // under another thread's launch by one that needs less
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(route_tile_smem(kMaxExperts, kMaxExperts)));
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kTileWarps * 32), smem, s, xt, W_g, b_g,
