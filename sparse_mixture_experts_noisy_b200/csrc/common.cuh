@@ -50,6 +50,11 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // once every CTA of this grid has called pdl_trigger(); pdl_wait() blocks until
 // the previous kernel on the stream has finished and its writes are visible
 // (a no-op for a kernel launched without the attribute).
+//
+// A kernel that uses tensor memory triggers behind its allocation and a barrier
+// of the block.  tcgen05.alloc waits without a limit: a dependent's CTA that came
+// to the SM first and took the columns would wait for this grid in pdl_wait(),
+// and this grid for the columns.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

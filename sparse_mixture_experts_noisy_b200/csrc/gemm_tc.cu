@@ -187,7 +187,6 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_tok, const __grid_constant
     const uint32_t tempty0 = smem_u32(&bars[2 * STAGES + 2]);
     const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -209,6 +208,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_tok, const __grid_constant
         tmem_alloc(smem_u32(&tmem_holder), TMEM_COLS);
         tmem_relinquish();
     }
+    __syncthreads();
+    pdl_trigger();  // behind the allocation: see common.cuh
     pdl_wait();
     for (int e = threadIdx.x; e < E; e += blockDim.x) cnt_s[e] = args.counts[e];
     __syncthreads();
@@ -466,7 +467,6 @@ tc2_gemm_kernel(const __grid_constant__ CUtensorMap tm_tok, const __grid_constan
     const uint32_t full0_lead = map_to_cta(full0, 0);
     const uint32_t tempty0_lead = map_to_cta(tempty0, 0);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -488,6 +488,8 @@ tc2_gemm_kernel(const __grid_constant__ CUtensorMap tm_tok, const __grid_constan
         tmem_alloc_pair(smem_u32(&tmem_holder), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    __syncthreads();
+    pdl_trigger();  // behind the allocation: see common.cuh
     pdl_wait();
     for (int e = threadIdx.x; e < E; e += blockDim.x) cnt_s[e] = args.counts[e];
     __syncthreads();
@@ -808,7 +810,6 @@ tc_wgrad_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant_
     const uint32_t tempty0 = smem_u32(&bars[2 * STAGES + 2]);
     const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -830,6 +831,8 @@ tc_wgrad_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant_
         tmem_alloc(smem_u32(&tmem_holder), TMEM_COLS);
         tmem_relinquish();
     }
+    __syncthreads();
+    pdl_trigger();  // behind the allocation: see common.cuh
     pdl_wait();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         cnt_s[e] = args.counts[e];
@@ -1063,7 +1066,6 @@ tc_wgrad2_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant
     const uint32_t full0_lead = map_to_cta(full0, 0);
     const uint32_t tempty0_lead = map_to_cta(tempty0, 0);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -1085,6 +1087,8 @@ tc_wgrad2_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant
         tmem_alloc_pair(smem_u32(&tmem_holder), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    __syncthreads();
+    pdl_trigger();  // behind the allocation: see common.cuh
     pdl_wait();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         cnt_s[e] = args.counts[e];

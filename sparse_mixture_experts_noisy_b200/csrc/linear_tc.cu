@@ -336,7 +336,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     const uint32_t drain = smem_u32(&bars[2 * kPairMaxStages + 4]);
     const uint32_t full0_lead = map_to_cta(full0, 0), tempty0_lead = map_to_cta(tempty0, 0);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -360,6 +359,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_constan
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before either signals the other
     tc_fence_after();
+    pdl_trigger();  // behind the allocation: see common.cuh
     const uint32_t tmem_base = tmem_holder;
     pdl_wait();
 
@@ -697,7 +697,6 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_consta
     const uint32_t tfull0 = smem_u32(&bars[2 * kMaxStages]), tempty0 = smem_u32(&bars[2 * kMaxStages + 2]);
     const uint32_t drain = smem_u32(&bars[2 * kMaxStages + 4]);
 
-    pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -720,6 +719,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_trigger();  // behind the allocation: see common.cuh
     const uint32_t tmem_base = tmem_holder;
     pdl_wait();
 
