@@ -170,6 +170,17 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
 }
 
 // ---------------------------------------------------------------- tcgen05
+// tcgen05.alloc waits without a limit for free columns, of which an SM has 512.
+// CTAs of a cluster hold theirs while they wait for one another, so two grids (on
+// two streams, or two clusters of one) could each hold what the other waits for.
+// Shared memory keeps them apart (228 KB an SM, 1 KB of it for each CTA): a CTA
+// of up to 256 columns asks for a third of it, so that two share an SM at most,
+// and one of more for so much that no other of these fits beside it.  Every launch
+// of a kernel with tensor memory holds to this.
+constexpr bool tmem_room(uint32_t cols, size_t dyn_smem) {
+    return dyn_smem >= (cols <= 256 ? 76u : 152u) * 1024u;
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(ncols)

@@ -735,6 +735,7 @@ cudaError_t launch_decode_fused(const void *x, const float *W_g, const float *b_
                 parts_up, parts_dn, rows * static_cast<int64_t>(d_ff), rows * static_cast<int64_t>(d), pieces, sync,
                 status, timeout_ns};
     constexpr size_t smem = static_cast<size_t>(kFStages) * kFSlot + 1024;
+    static_assert(tmem_room(kFTmemCols, smem), "tensor memory");
     e = cudaFuncSetAttribute(decode_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -714,6 +714,7 @@ cudaError_t launch_tc(const void *tok, int64_t tok_rows, const void *W, int E, i
     if (!make_tmap_bf16_2d(&tm_tok, tok, tok_rows, K, SWAP ? BN : kBM)) return cudaErrorInvalidValue;
     if (!make_tmap_bf16_3d(&tm_w, W, E, Nw, K, SWAP ? kBM : BN)) return cudaErrorInvalidValue;
     constexpr int smem = STAGES * (kBM + BN) * kBK * 2 + 1024;
+    static_assert(tmem_room(tmem_cols<BN>(), smem), "tensor memory");
     auto kern = tc_gemm_kernel<BN, SWAP, EPI, STAGES>;
     // every call: the attribute belongs to the current device's context
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -736,6 +737,7 @@ cudaError_t launch_tc2(const void *tok, int64_t tok_rows, const void *W, int E, 
         if (!make_tmap_bf16_3d(&tm_w, W, E, Nw, K, 128)) return cudaErrorInvalidValue;
     }
     constexpr int smem = STAGES * 2 * 128 * kBK * 2 + 1024;
+    static_assert(tmem_room(512, smem), "tensor memory");
     auto kern = tc2_gemm_kernel<EPI, STAGES, B_MN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1303,6 +1305,7 @@ cudaError_t launch_wgrad(const void *P, const void *Q, int64_t rows, int M, int 
     if (!make_tmap_bf16_2d(&tm_p, P, rows, M, 64)) return cudaErrorInvalidValue;
     if (!make_tmap_bf16_2d(&tm_q, Q, rows, Nn, 64)) return cudaErrorInvalidValue;
     constexpr int smem = STAGES * (kWM + kWN) * kBK * 2 + 1024;
+    static_assert(tmem_room(2 * kWN, smem), "tensor memory");
     auto kern = tc_wgrad_kernel<STAGES>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1311,6 +1314,7 @@ cudaError_t launch_wgrad(const void *P, const void *Q, int64_t rows, int M, int 
         // CTA pairs, 256 x 256 tiles
         constexpr int STAGES2 = 6;
         constexpr int smem2 = STAGES2 * 2 * 128 * kBK * 2 + 1024;
+        static_assert(tmem_room(512, smem2), "tensor memory");
         auto kern2 = tc_wgrad2_kernel<STAGES2>;
         e = cudaFuncSetAttribute(kern2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
         if (e != cudaSuccess) return e;

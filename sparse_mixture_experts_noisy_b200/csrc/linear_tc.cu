@@ -600,6 +600,9 @@ constexpr int kSplitThreads = 192;
 constexpr int split_ctas(bool fp32) { return fp32 ? 1 : 2; }
 constexpr int kSplitSmem = 216 * 1024;
 
+// Columns of one accumulator, and of the two that a CTA has.
+template <int BN> constexpr int split_acc_cols() { return BN < 32 ? 32 : BN; }
+template <int BN> constexpr uint32_t split_tmem_cols() { return 2 * split_acc_cols<BN>(); }
 template <int BN> constexpr int split_b_bytes(bool mn) { return (mn && BN < 64 ? 64 : BN) * kBK * 2; }
 template <typename T, int BN> constexpr int split_stage_bytes(bool mn) {
     return (sizeof(T) == 4 ? 3 : 1) * (128 * kBK * 2 + split_b_bytes<BN>(mn));
@@ -618,7 +621,8 @@ template <typename T, int BN> constexpr int split_smem(int stage_bytes) {
 // this one whatever the call needs: it belongs to the kernel, and a call that set
 // a smaller one would take it from under another thread's launch.
 template <typename T, int BN> constexpr int split_smem_limit() {
-    const int k = split_smem<T, BN>(split_stage_bytes<T, BN>(false)), mn = split_smem<T, BN>(split_stage_bytes<T, BN>(true));
+    constexpr int k = split_smem<T, BN>(split_stage_bytes<T, BN>(false)), mn = split_smem<T, BN>(split_stage_bytes<T, BN>(true));
+    static_assert(tmem_room(split_tmem_cols<BN>(), k < mn ? k : mn), "tensor memory");
     return k > mn ? k : mn;
 }
 
@@ -670,8 +674,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tp0, const __grid_consta
                     const __grid_constant__ SplitArgs args) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PLANES = SPLIT ? 3 : 1, TERMS = SPLIT ? kTerms : 1;
-    constexpr int COLS = BN < 32 ? 32 : BN;  // tensor-memory columns of one accumulator
-    constexpr uint32_t TMEM_COLS = 2 * COLS;
+    constexpr int COLS = split_acc_cols<BN>();
+    constexpr uint32_t TMEM_COLS = split_tmem_cols<BN>();
     constexpr uint32_t A_BYTES = 128 * kBK * 2;
     constexpr int kMaxStages = kSplitMaxStages;
     const int S = args.S, stages = args.stages;
@@ -989,6 +993,7 @@ cudaError_t launch_pair(const TcProduct *t, int count, uint64_t timeout_ns, int 
     constexpr int PLANES = SPLIT ? 3 : 1;
     auto kern = linear_pair_kernel<T, FULL>;
     constexpr int smem = kPairRing + 1024;
+    static_assert(tmem_room(512, smem), "tensor memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // pairs that fit the device at once, asked for once per device

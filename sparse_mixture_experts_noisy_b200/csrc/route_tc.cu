@@ -749,7 +749,9 @@ cudaError_t launch_cluster_t(const CUtensorMap &tm, const CUtensorMap &tw, Route
     const int ld = a.E + 1 + (a.E & 1);
     const size_t part_bytes = align_up(static_cast<size_t>(kRM) * ld * sizeof(float), 16);
     if (part_bytes + static_cast<size_t>(kRM) * a.k * sizeof(float) > ring) return cudaErrorInvalidValue;
-    const size_t smem = ring + 1024;
+    // E > 128: one stage of 118 KB, and all of tensor memory; the CTA keeps the SM
+    // to itself (two of them never fitted)
+    const size_t smem = tmem_room(route_tmem_cols<UPT>(), ring + 1024) ? ring + 1024 : kRpSmemBudget;
     a.stages = stages;
     a.pick_off = static_cast<int>(part_bytes);
     auto kern = route_tc_kernel<UPT, PRE>;
@@ -788,6 +790,7 @@ cudaError_t launch_persistent_t(const CUtensorMap &tm, const CUtensorMap &tw, Ro
     if (stages > kRMaxStages) stages = kRMaxStages;
     const size_t ring = static_cast<size_t>(stages) * STAGE;
     const size_t smem = ring + fixed;
+    if (!tmem_room(routep_tmem_cols<UPT>(), smem)) return cudaErrorInvalidValue;
     a.stages = stages;
     a.pick_off = static_cast<int>(ring);
     a.list_off = static_cast<int>(ring + pick_bytes);

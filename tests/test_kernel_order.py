@@ -44,3 +44,11 @@ def test_dependents_start_behind_the_allocation(file, name, body):
     for m in re.finditer(r"pdl_trigger\(\)", body):
         # a barrier of the block lies between: every warp's trigger is behind warp 1's allocation
         assert m.start() > alloc and "__syncthreads()" in body[alloc:m.start()], (file, name)
+
+
+@pytest.mark.parametrize("file", sorted({f for f, _, _ in FOUND}))
+def test_launches_keep_room_for_tensor_memory(file):
+    """Every launch of such a kernel is held to tmem_room(), so that no SM gets
+    CTAs that need more than its 512 columns together."""
+    text = re.sub(r"//[^\n]*", "", open(next(f for f in SOURCES if f.endswith(os.sep + file)), encoding="utf-8").read())
+    assert text.count("tmem_room(") >= sum(f == file for f, _, _ in FOUND)
