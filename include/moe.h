@@ -376,9 +376,9 @@ MOE_API moe_status moe_backward(const void *x, moe_dtype dt, const float *W_g, c
  *  y            device [N, d] of dt out
  *  sum_out      device [N, d] of dt out: h; required with a residual, else NULL
  *  mean, rstd   device [N] fp32 out, each nullable
- * y or sum_out (not both) may be the array x or residual itself; no other
- * overlap.  Any 1 <= d <= 2^30; rows may start at any multiple of the element
- * size. */
+ * y or sum_out may be the array x or residual itself; any other overlap of an
+ * output with an input or another output is refused.  Any 1 <= d <= 2^30; the
+ * arrays start on 16 bytes, their rows at any multiple of the element size. */
 MOE_API moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, const float *gamma,
                                   const float *beta, float eps, int64_t N, int d, void *y, void *sum_out,
                                   float *mean, float *rstd, void *stream);
@@ -394,6 +394,7 @@ MOE_API moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype
  *  dx           device [N, d] of dt out; may be the array dy, h or dres itself
  *  dgamma, dbeta  device [d] fp32 out (overwritten; zeros for N = 0), each nullable
  *  ws           scratch of moe_layer_norm_backward_workspace_size() bytes
+ * Any other overlap of an output or ws with an input or one another is refused.
  * Deterministic: no atomics decide a sum's order. */
 MOE_API size_t moe_layer_norm_backward_workspace_size(int64_t N, int d, moe_dtype dt);
 MOE_API moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, const float *gamma,
@@ -412,12 +413,12 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dt
  *  y         device [N, d_out] of dt out, rounded once
  *  z_out     device [N, d_out] of dt out, nullable: z rounded, for moe_linear_backward
  *  ws        scratch of moe_linear_workspace_size() bytes (NULL if that is 0)
- * 1 <= d_in, d_out <= 2^30.  No other overlap of outputs and inputs.  fp32
- * accumulation.  fp32 storage keeps fp32's precision (products of three bf16
- * parts on the tensor cores, or fp32 on CUDA cores for a few tokens) for finite
- * values below 3.38e38; an infinite one gives NaN.  A wait of its kernels that
- * runs out is recorded in the library's own per-device word:
- * moe_check_linear_status(). */
+ * 1 <= d_in, d_out <= 2^30.  Any other overlap of an output or ws with an input
+ * or one another is refused.  fp32 accumulation.  fp32 storage keeps fp32's
+ * precision (products of three bf16 parts on the tensor cores, or fp32 on CUDA
+ * cores for a few tokens) for finite values below 3.38e38; an infinite one gives
+ * NaN.  A wait of its kernels that runs out is recorded in the library's own
+ * per-device word: moe_check_linear_status(). */
 MOE_API size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt);
 MOE_API moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b, int activation,
                               const void *residual, int64_t N, int d_in, int d_out, void *y, void *z_out, void *ws,
@@ -433,7 +434,8 @@ MOE_API moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const 
  *  db        device [d_out] fp32 out, nullable; overwritten, zeros for N = 0
  *  ws        scratch of moe_linear_backward_workspace_size() bytes
  * dZ is rounded to dt before the two products, db sums it unrounded in fp32.
- * The outputs may not overlap the inputs.  Deterministic. */
+ * An output or ws that overlaps an input or another output is refused.
+ * Deterministic. */
 MOE_API size_t moe_linear_backward_workspace_size(int64_t N, int d_in, int d_out, int activation, moe_dtype dt);
 MOE_API moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, const void *W, const void *z,
                                        int activation, int64_t N, int d_in, int d_out, void *dx, void *dW, float *db,

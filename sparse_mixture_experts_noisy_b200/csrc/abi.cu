@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -98,6 +99,32 @@ moe_status linear_sms(int &sms) {
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? cuda_fail(e, "device query")
                             : fail(MOE_ERR_CUDA, "device query: the dense layer needs a device of two SMs (got %d)", sms);
+}
+
+// An array of a call.
+struct Span {
+    const void *p;
+    size_t bytes;
+    const char *name;
+};
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(a.p), v = reinterpret_cast<uintptr_t>(b.p);
+    if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+    return u <= v ? v - u < a.bytes : u - v < b.bytes;
+}
+// Refuses an output that overlaps an input or another output.  `over`: the inputs
+// that an output of index < n_over may be in whole (the same array), by index.
+moe_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins, int n_over = 0,
+                       unsigned over = 0u) {
+    const Span *o = outs.begin(), *q = ins.begin();
+    for (size_t i = 0; i < outs.size(); ++i) {
+        for (size_t j = 0; j < ins.size(); ++j)
+            if (overlap(o[i], q[j]) && !(static_cast<int>(i) < n_over && ((over >> j) & 1u) && o[i].p == q[j].p))
+                return fail(MOE_ERR_INVALID_ARG, "%s must not overlap %s", o[i].name, q[j].name);
+        for (size_t j = i + 1; j < outs.size(); ++j)
+            if (overlap(o[i], o[j])) return fail(MOE_ERR_INVALID_ARG, "%s must not overlap %s", o[i].name, o[j].name);
+    }
+    return MOE_OK;
 }
 
 #define REQUIRE_PTR(p, name)                                                                    \
@@ -668,6 +695,12 @@ moe_status moe_layer_norm(const void *x, const void *residual, moe_dtype dt, con
     if (residual == nullptr && sum_out != nullptr)
         return fail(MOE_ERR_INVALID_ARG, "sum_out must be NULL without a residual (the sum is x)");
     if (N > 0 && sum_out == y) return fail(MOE_ERR_INVALID_ARG, "y and sum_out must be different arrays");
+    const size_t rows = static_cast<size_t>(N) * d * elem_bytes(dt), cols = sizeof(float) * static_cast<size_t>(d),
+                 per_row = sizeof(float) * static_cast<size_t>(N);
+    // y and sum_out may be x or the residual: a thread reads its elements before it writes them
+    st = check_apart({{y, rows, "y"}, {sum_out, rows, "sum_out"}, {mean, per_row, "mean"}, {rstd, per_row, "rstd"}},
+                     {{x, rows, "x"}, {residual, rows, "residual"}, {gamma, cols, "gamma"}, {beta, cols, "beta"}}, 2, 3u);
+    if (st != MOE_OK) return st;
     cudaError_t e = moe::launch_norm(x, residual, dt == MOE_BF16 ? 1 : 0, gamma, beta, eps, N, d, y, sum_out, mean,
                                      rstd, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "layer norm launch");
@@ -700,6 +733,12 @@ moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dtype dt, 
         return fail(MOE_ERR_WORKSPACE, "layer norm backward workspace needs %zu bytes (got %zu)", need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     REQUIRE_PTR(ws, "ws");
+    const size_t rows = static_cast<size_t>(N) * d * elem_bytes(dt), cols = sizeof(float) * static_cast<size_t>(d),
+                 per_row = sizeof(float) * static_cast<size_t>(N);
+    st = check_apart({{dx, rows, "dx"}, {dgamma, cols, "dgamma"}, {dbeta, cols, "dbeta"}, {ws, need, "ws"}},
+                     {{dy, rows, "dy"}, {h, rows, "h"}, {dres, rows, "dres"}, {gamma, cols, "gamma"},
+                      {mean, per_row, "mean"}, {rstd, per_row, "rstd"}}, 1, 7u);
+    if (st != MOE_OK) return st;
     cudaError_t e = moe::launch_norm_bwd(dy, h, dt == MOE_BF16 ? 1 : 0, gamma, mean, rstd, dres, N, d, dx, dgamma,
                                          dbeta, ws, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
@@ -732,6 +771,12 @@ moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b
                     ws == nullptr ? (size_t)0 : ws_bytes);
     OPTIONAL_PTR(ws, "ws");
     if (N == 0) return MOE_OK;
+    const size_t in = static_cast<size_t>(N) * d_in * elem_bytes(dt), out = static_cast<size_t>(N) * d_out * elem_bytes(dt),
+                 weights = static_cast<size_t>(d_out) * d_in * elem_bytes(dt);
+    st = check_apart({{y, out, "y"}, {z_out, out, "z_out"}, {ws, need, "ws"}},
+                     {{residual, out, "residual"}, {x, in, "x"}, {W, weights, "W"},
+                      {b, sizeof(float) * static_cast<size_t>(d_out), "b"}}, 1, 1u);
+    if (st != MOE_OK) return st;
     int sms = 0;
     if ((st = linear_sms(sms)) != MOE_OK) return st;
     moe::LinearArgs a{x, dt == MOE_BF16 ? 1 : 0, W, b, activation, residual, N, d_in, d_out, y, z_out};
@@ -768,6 +813,13 @@ moe_status moe_linear_backward(const void *dy, const void *x, moe_dtype dt, cons
         return fail(MOE_ERR_WORKSPACE, "linear backward workspace needs %zu bytes (got %zu)", need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     OPTIONAL_PTR(ws, "ws");
+    const size_t in = static_cast<size_t>(N) * d_in * elem_bytes(dt), out = static_cast<size_t>(N) * d_out * elem_bytes(dt),
+                 weights = static_cast<size_t>(d_out) * d_in * elem_bytes(dt);
+    st = check_apart({{dx, in, "dx"}, {dW, weights, "dW"}, {db, sizeof(float) * static_cast<size_t>(d_out), "db"},
+                      {ws, need, "ws"}},
+                     {{dy, out, "dy"}, {x, in, "x"}, {W, weights, "W"},
+                      {z, activation != MOE_ACT_NONE ? out : 0, "z"}});
+    if (st != MOE_OK) return st;
     int sms = 0;
     if ((st = linear_sms(sms)) != MOE_OK) return st;
     moe::LinearBwdArgs a{dy, x, dt == MOE_BF16 ? 1 : 0, W, z, activation, N, d_in, d_out, dx, dW, db};
