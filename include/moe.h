@@ -414,11 +414,14 @@ MOE_API moe_status moe_layer_norm_backward(const void *dy, const void *h, moe_dt
  *  z_out     device [N, d_out] of dt out, nullable: z rounded, for moe_linear_backward
  *  ws        scratch of moe_linear_workspace_size() bytes (NULL if that is 0)
  * 1 <= d_in, d_out <= 2^30.  Any other overlap of an output or ws with an input
- * or one another is refused.  fp32 accumulation.  fp32 storage keeps fp32's
- * precision (products of three bf16 parts on the tensor cores, or fp32 on CUDA
- * cores for a few tokens) for finite values below 3.38e38; an infinite one gives
- * NaN.  A wait of its kernels that runs out is recorded in the library's own
- * per-device word: moe_check_linear_status(). */
+ * or one another is refused.
+ * fp32 accumulation.  fp32 storage runs on CUDA cores in fp32 for a few tokens (16;
+ * up to 64 of a small W) and else as products of three bf16 parts of each value on
+ * the tensor cores.  The parts keep all bits of finite values of 2^-110 (7.7e-34)
+ * and above; a smaller one enters with an error of 2^-134 at most.  An infinite
+ * value gives NaN there, and the infinities of fp32 on the CUDA cores.
+ * A wait of its kernels that runs out is recorded in the library's own per-device
+ * word: moe_check_linear_status(). */
 MOE_API size_t moe_linear_workspace_size(int64_t N, int d_in, int d_out, moe_dtype dt);
 MOE_API moe_status moe_linear(const void *x, moe_dtype dt, const void *W, const float *b, int activation,
                               const void *residual, int64_t N, int d_in, int d_out, void *y, void *z_out, void *ws,

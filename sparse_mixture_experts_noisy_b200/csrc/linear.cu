@@ -14,10 +14,14 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- operands for the tensor cores
-// v = p0 + p1 + p2 in bf16 parts (each the rest rounded to bf16; the rests are
-// exact in fp32).  A value above bf16's largest, 3.39e38, has no such parts.
+// v = p0 + p1 + p2 in bf16 parts, each the rest rounded to bf16 (the rests are
+// exact in fp32).  The sum is v for |v| >= 2^-110; below, the last part ends at
+// bf16's smallest step and the sum is off by 2^-134 at most.  p0 stays at bf16's
+// largest, 3.39e38, for the finite values above it.  An infinite v has no parts:
+// they come out as infinite and NaN, and so its products as NaN.
 __device__ __forceinline__ void bf16_parts(float v, __nv_bfloat16 (&p)[3]) {
-    p[0] = __float2bfloat16_rn(v);
+    constexpr float kMost = 3.38953139e38f;  // bf16 0x7f7f
+    p[0] = __float2bfloat16_rn(fminf(fmaxf(v, -kMost), kMost));
     v -= __bfloat162float(p[0]);
     p[1] = __float2bfloat16_rn(v);
     v -= __bfloat162float(p[1]);
