@@ -510,6 +510,8 @@ MOE_API moe_status moe_check_status(void *ws, void *stream, uint32_t *detail);
  * can check that a wait which runs out ends cleanly and that its report
  * survives later calls on the same workspace. */
 MOE_API moe_status moe_debug_wait_timeout(uint32_t timeout_us, void *ws, size_t ws_bytes, void *stream);
+/* The same for the dense layer's word on the current device (moe_check_linear_status). */
+MOE_API moe_status moe_debug_linear_wait_timeout(uint32_t timeout_us, void *stream);
 
 /* Number of streaming multiprocessors the library sizes its persistent grids
  * for on the current device (0 if no device). */

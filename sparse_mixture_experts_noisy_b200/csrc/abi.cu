@@ -996,4 +996,15 @@ moe_status moe_debug_wait_timeout(uint32_t timeout_us, void *ws, size_t ws_bytes
     return MOE_OK;
 }
 
+moe_status moe_debug_linear_wait_timeout(uint32_t timeout_us, void *stream) {
+    if (timeout_us == 0 || timeout_us > 2000000u)
+        return fail(MOE_ERR_INVALID_ARG, "timeout_us must be in [1, 2000000]");
+    uint32_t *word = nullptr;
+    cudaError_t e = moe::linear_status_address(&word);
+    if (e == cudaSuccess)
+        e = moe::launch_wait_timeout(word, static_cast<uint64_t>(timeout_us) * 1000ull, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "wait-timeout diagnostic launch");
+    return MOE_OK;
+}
+
 }  // extern "C"

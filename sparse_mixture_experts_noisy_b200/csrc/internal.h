@@ -214,5 +214,6 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
 // Reads and clears (on stream s, then synchronises it) the status word of the
 // dense layer's kernels on the current device.
 cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s);
+cudaError_t linear_status_address(uint32_t **word);
 
 }  // namespace moe

@@ -34,6 +34,10 @@ namespace moe {
 // The dense layer's status word on each device (bounded waits of its kernels).
 static __device__ uint32_t g_linear_status;
 
+cudaError_t linear_status_address(uint32_t **word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_linear_status);
+}
+
 cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
     cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
     if (e != cudaSuccess) return e;

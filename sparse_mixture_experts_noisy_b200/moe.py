@@ -32,7 +32,8 @@ EXPORTS = ("moe_capacity", "moe_gathered_rows", "moe_route", "moe_route_ex", "mo
            "moe_linear_workspace_size", "moe_linear", "moe_linear_backward_workspace_size", "moe_linear_backward",
            "moe_check_linear_status",
            "moe_workspace_size", "moe_forward", "moe_forward_ex", "moe_forward_launches",
-           "moe_set_fused_small_batch", "moe_check_status", "moe_debug_wait_timeout", "moe_num_sms", "moe_last_error")
+           "moe_set_fused_small_batch", "moe_check_status", "moe_debug_wait_timeout", "moe_debug_linear_wait_timeout",
+           "moe_num_sms", "moe_last_error")
 
 
 class MoeError(RuntimeError):
@@ -97,6 +98,7 @@ def load_library(path: str = LIB_PATH):
             "moe_set_fused_small_batch": (I, [I]),
             "moe_check_status": (I, [P, P, ctypes.POINTER(U32)]),
             "moe_debug_wait_timeout": (I, [U32, P, SZ, P]),
+            "moe_debug_linear_wait_timeout": (I, [U32, P]),
             "moe_num_sms": (I, []),
             "moe_last_error": (ctypes.c_char_p, []),
         }
@@ -621,6 +623,11 @@ def check_status(ws, stream=None):
 
 def debug_wait_timeout(timeout_us: int, ws, stream=None):
     _check(load_library().moe_debug_wait_timeout(int(timeout_us), _p(ws), ws.numel(), _stream(stream)))
+
+
+def debug_linear_wait_timeout(timeout_us: int, stream=None):
+    """A wait that runs out, reported into the dense layer's word (check_linear_status)."""
+    _check(load_library().moe_debug_linear_wait_timeout(int(timeout_us), _stream(stream)))
 
 
 class MoELayer:

@@ -19,6 +19,7 @@ CALLS = {
     "expert_ffn": "L.moe_expert_ffn(A, B, C, D, E, DT, 128, 64, 64, 8, F, W, BIG, None)",
     "forward": "L.moe_forward(A, DT, B, None, None, 0.0, N, 64, 8, 64, 2, 1.0, C, D, E, None, None, None, None, None,"
                " W, BIG, None)",
+    "debug_linear_wait_timeout": "L.moe_debug_linear_wait_timeout(10, None)",
     "check_linear_status": "L.moe_check_linear_status(None, None)",
 }
 
@@ -39,6 +40,14 @@ for DT in (0, 1):
         assert L.moe_last_error()
 print("refused")
 """
+
+
+def test_wait_diagnostic_limits():
+    from sparse_mixture_experts_noisy_b200 import moe
+    from sparse_mixture_experts_noisy_b200.build import build
+    build()
+    for us in (0, 2000001):
+        assert moe.load_library().moe_debug_linear_wait_timeout(us, None) == 1
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
