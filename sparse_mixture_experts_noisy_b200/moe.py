@@ -676,13 +676,17 @@ class MoEBlock:
     own.  After the last block, moe_layer_norm(s, ..., residual=m).
 
     gamma, beta: [d] fp32 (None: 1, 0).  shared: (W1 [d_s, d], b1, W2 [d, d_s],
-    b2), the biases fp32 or None.  Runs on the current stream."""
+    b2), the biases fp32 or None.  Runs on the current stream of x's device."""
 
     def __init__(self, layer: MoELayer, gamma=None, beta=None, eps=1e-5, shared=None, shared_act=ACT_RELU):
         self.layer, self.gamma, self.beta, self.eps = layer, gamma, beta, float(eps)
         self.shared, self.shared_act = shared, int(shared_act)
 
     def __call__(self, x, delta=None, noise=None):
+        _cuda(x, "x")
+        if (at := _elsewhere(x, None)) is not None:
+            with at:
+                return self(x, delta, noise)
         n, h, _, _ = moe_layer_norm(x, self.gamma, self.beta, self.eps, residual=delta)
         m = self.layer(n, noise=noise)
         if self.shared is None:
@@ -697,6 +701,10 @@ class MoEBlock:
         L = self.layer
         if L.act != ACT_RELU or L.b_up is not None or L.b_down is not None:
             raise ValueError("training needs ReLU experts without biases")
+        _cuda(x, "x")
+        if (at := _elsewhere(x, None)) is not None:
+            with at:
+                return self.train(x, delta, noise)
         n, h, mean, rstd = moe_layer_norm(x, self.gamma, self.beta, self.eps, residual=delta, want_stats=True)
         topk, gates, _ = moe_route(n, L.W_g, L.k, b_g=L.b_g, noise=noise, sigma=L.sigma, want_logits=False)
         d = moe_dispatch(topk, n, L.E, L.cf)
@@ -714,6 +722,9 @@ class MoEBlock:
         """Gradients for those of s and m -> dict(dx (of x and delta alike),
         dgamma, dbeta, dW_g, db_g, dW_up, dW_down, and with a shared expert dW1,
         db1, dW2, db2)."""
+        if (at := _elsewhere(saved["h"], None)) is not None:
+            with at:
+                return self.backward(ds, dm, saved)
         L, v, d = self.layer, saved, saved["dispatch"]
         g = moe_backward(v["n"], L.W_g, L.W_up, L.W_down, L.k, v["topk"], v["gates"], d["slot"], d["offsets"],
                          d["counts"], d["x_gathered"], v["H"], v["out"], dm)
@@ -724,6 +735,8 @@ class MoEBlock:
             second = moe_linear_backward(ds, v["u"], W2)
             first = moe_linear_backward(second["dx"], v["n"], W1, act=self.shared_act, z=v["z"])
             g.update(dW1=first["dW"], db1=first["db"], dW2=second["dW"], db2=second["db"])
+            # n's two gradients, each rounded to its type, and their sum once more: in
+            # bf16 half a step, what the norm's input gradient is rounded by anyway
             dn = dn.add_(first["dx"])
         g.update(moe_layer_norm_backward(dn, v["h"], v["mean"], v["rstd"], gamma=self.gamma, dres=ds, dx=dn))
         return g
