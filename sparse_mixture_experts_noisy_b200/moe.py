@@ -7,6 +7,8 @@ built, or no CUDA device is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import math
 import os
 import threading
@@ -169,6 +171,45 @@ def route_workspace(d, E, device):
     return new_workspace(load_library().moe_route_workspace_size(d, E), device)
 
 
+def _elsewhere(x, stream):
+    """None when a call can run as it stands: no stream given, x on the current
+    device.  Otherwise the context in which its outputs are allocated and its
+    kernels launched: x's device, and `stream`, which must be of that device."""
+    if stream is None:
+        if x.get_device() == torch._C._cuda_getDevice():
+            return None
+        return torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _on_stream(f):
+    """f on its tensors' device with `stream` as the current stream: what it
+    allocates then belongs to the stream that its kernels run on, and a scratch
+    array that f drops is not handed out again while they use it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                break
+        else:
+            return f(*args, **kwargs)   # nothing on a device: f says what is wrong
+        if len(args) > at:
+            stream, args = args[at], args[:at] + (None,) + args[at + 1:]
+        else:
+            stream = kwargs.pop("stream", None)
+        if (where := _elsewhere(t, stream)) is None:
+            return f(*args, **kwargs)
+        with where:
+            return f(*args, **kwargs)
+
+    return call
+
+
+@_on_stream
 def moe_route(x, W_g, k, b_g=None, noise=None, sigma=0.0, want_logits=True, stream=None, status=None):
     """-> (topk_idx [N,k] int32, gates [N,k] fp32, logits [N,E] fp32 or None).
     status (a workspace, nullable): its first 4 bytes record a router timeout
@@ -198,6 +239,7 @@ def check_route_status(stream=None):
     return int(code), int(word.value)
 
 
+@_on_stream
 def moe_dispatch(topk_idx, x, E, cf, stream=None):
     """-> dict(slot, counts, offsets, x_gathered, rows, C)."""
     L = load_library()
@@ -221,6 +263,7 @@ def moe_dispatch(topk_idx, x, E, cf, stream=None):
                 C=capacity(N, E, k, cf))
 
 
+@_on_stream
 def moe_dispatch_noalloc(topk_idx, x, E, cf, stream=None):
     """moe_dispatch for callers that cannot allocate device memory at dispatch
     time: the library's fixed scratch array replaces the workspace.  The
@@ -246,6 +289,7 @@ def moe_dispatch_noalloc(topk_idx, x, E, cf, stream=None):
                 C=capacity(N, E, k, cf))
 
 
+@_on_stream
 def moe_shard_count(topk_idx, E, ws, stream=None):
     """This shard's [k, E] int32 counts of j-th choices per expert (device).
     `ws` (from shard_workspace) must then go, untouched, to moe_shard_dispatch."""
@@ -261,6 +305,7 @@ def shard_workspace(N_local, E, k, device):
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def moe_shard_base(all_counts, rank, stream=None):
     """all_counts [G, k, E] int32 (device, rank order) -> base [k, E] int32."""
     L = load_library()
@@ -270,6 +315,7 @@ def moe_shard_base(all_counts, rank, stream=None):
     return base
 
 
+@_on_stream
 def moe_shard_dispatch(topk_idx, x, E, C, counts_je, base, ws, stream=None):
     """-> dict(slot, counts, offsets, x_gathered, rows) for this shard."""
     L = load_library()
@@ -286,6 +332,7 @@ def moe_shard_dispatch(topk_idx, x, E, C, counts_je, base, ws, stream=None):
     return dict(slot=slot, counts=counts, offsets=offsets, x_gathered=xg, rows=rows)
 
 
+@_on_stream
 def moe_expert_ffn(x_gathered, offsets, counts, W_up, W_down, stream=None, ws=None, out=None, act=ACT_RELU,
                    b_up=None, b_down=None):
     """-> out_gathered [rows, d] (rows outside the kept ranges unspecified).
@@ -310,6 +357,7 @@ def moe_expert_ffn(x_gathered, offsets, counts, W_up, W_down, stream=None, ws=No
     return out
 
 
+@_on_stream
 def moe_expert_ffn_train(x_gathered, offsets, counts, W_up, W_down, stream=None, ws=None):
     """Expert FFN that keeps the hidden activations for the backward.
     -> (out_gathered [rows, d], H [rows, d_ff])."""
@@ -329,6 +377,7 @@ def moe_expert_ffn_train(x_gathered, offsets, counts, W_up, W_down, stream=None,
     return out, H
 
 
+@_on_stream
 def moe_backward(x, W_g, W_up, W_down, k, topk_idx, gates, slot, offsets, counts, x_gathered, H, out_gathered, dy,
                  stream=None, ws=None):
     """Gradients of sum(dy * y) for the routing of a staged forward.
@@ -358,6 +407,7 @@ def moe_backward(x, W_g, W_up, W_down, k, topk_idx, gates, slot, offsets, counts
     return out
 
 
+@_on_stream
 def moe_combine(out_gathered, slot, topk_idx, offsets, gates, stream=None, y=None):
     """-> y [N, d]."""
     L = load_library()
@@ -370,6 +420,7 @@ def moe_combine(out_gathered, slot, topk_idx, offsets, gates, stream=None, y=Non
     return y
 
 
+@_on_stream
 def moe_load_stats(topk_idx, E, cf, gates=None, stream=None):
     """Per-expert load of a routed batch (slide 14's used_capacity and more).
     -> dict(load [E] int32, used [E] int32, importance [E] float64 or None)."""
@@ -388,19 +439,6 @@ def moe_load_stats(topk_idx, E, cf, gates=None, stream=None):
 
 
 _F32 = torch.float32
-
-
-def _elsewhere(x, stream):
-    """None when a call can run as it stands: no stream given, x on the current
-    device.  Otherwise the context in which its outputs are allocated and its
-    kernels launched: x's device, and `stream`, which must be of that device."""
-    if stream is None:
-        if x.get_device() == torch._C._cuda_getDevice():
-            return None
-        return torch.cuda.device(x.device)
-    if stream.device != x.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-    return torch.cuda.stream(stream)
 
 
 def _current(index):
@@ -580,6 +618,7 @@ def set_fused_small_batch(on: bool | None) -> bool:
     return bool(load_library().moe_set_fused_small_batch(-1 if on is None else int(bool(on))))
 
 
+@_on_stream
 def moe_forward(x, W_g, W_up, W_down, k, cf, b_g=None, noise=None, sigma=0.0, y=None, ws=None,
                 intermediates=False, stream=None, act=ACT_RELU, b_up=None, b_down=None):
     """The whole layer.  -> y, or (y, dict of logits/topk_idx/gates/slot/counts).
@@ -655,6 +694,7 @@ class MoELayer:
     def workspace(self):
         return self._ws
 
+    @_on_stream
     def __call__(self, x, noise=None, y=None, stream=None):
         if self._ws is None or x.shape[0] != self._ws_tokens:
             self._reserve(x.shape[0], x.dtype)
