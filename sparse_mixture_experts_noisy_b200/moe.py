@@ -671,7 +671,10 @@ def debug_linear_wait_timeout(timeout_us: int, stream=None):
 
 class MoELayer:
     """Weights resident on the device plus a reusable workspace; __call__ runs
-    moe_forward on the current stream without allocating."""
+    moe_forward on the current stream without allocating.  A larger batch takes a
+    larger workspace; one that a graph was captured with stays the layer's.  Calls
+    and replays share it, so they follow one another: on one stream, or ordered by
+    events."""
 
     def __init__(self, W_g, W_up, W_down, k, cf, b_g=None, sigma=0.0, max_tokens=None, act=ACT_RELU,
                  b_up=None, b_down=None):
@@ -681,6 +684,7 @@ class MoELayer:
         self.E, self.d_ff, self.d = W_up.shape
         self._ws = None
         self._ws_tokens = -1
+        self._captured = []   # workspaces whose addresses are in a graph: never given back
         if max_tokens is not None:
             self._reserve(max_tokens, W_up.dtype)
 
@@ -698,6 +702,8 @@ class MoELayer:
     def __call__(self, x, noise=None, y=None, stream=None):
         if self._ws is None or x.shape[0] != self._ws_tokens:
             self._reserve(x.shape[0], x.dtype)
+        if torch.cuda.is_current_stream_capturing() and not any(w is self._ws for w in self._captured):
+            self._captured.append(self._ws)
         return moe_forward(x, self.W_g, self.W_up, self.W_down, self.k, self.cf, b_g=self.b_g,
                            noise=noise, sigma=self.sigma, y=y, ws=self._ws, stream=stream, act=self.act,
                            b_up=self.b_up, b_down=self.b_down)
@@ -789,7 +795,7 @@ class GraphedForward:
     allocates nothing, so the whole forward replays as one graph launch.  Copy
     new inputs into `.x` (and `.noise`) before `replay()`; the output lands in
     `.y`.  The graph bakes in the buffers' addresses: keep this object (and
-    the layer's weights and workspace) alive while replaying."""
+    the layer's weights) alive while replaying."""
 
     def __init__(self, layer: MoELayer, x, noise=None):
         self.layer = layer

@@ -67,6 +67,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(moe, "load_library", lambda *a: lib)
     monkeypatch.setattr(moe, "_elsewhere", lambda t, stream: None if stream is None else Switch())
     monkeypatch.setattr(moe, "_stream", lambda stream: "current" if stream is None else stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     empty = torch.empty
 
     def note(*a, **k):
