@@ -968,14 +968,9 @@ int moe_set_fused_small_batch(int on) {
 
 moe_status moe_check_status(void *ws, void *stream, uint32_t *detail) {
     if (ws == nullptr) return fail(MOE_ERR_INVALID_ARG, "ws must not be NULL");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint32_t word = 0;
-    cudaError_t e = cudaMemcpyAsync(&word, ws, sizeof word, cudaMemcpyDeviceToHost, s);
+    cudaError_t e = moe::status_read_clear(static_cast<uint32_t *>(ws), &word, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "status read");
-    e = cudaMemsetAsync(ws, 0, sizeof word, s);
-    if (e != cudaSuccess) return cuda_fail(e, "status clear");
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
     if (detail) *detail = word;
     if (word & moe::ST_TIMEOUT)
         return fail(MOE_ERR_TIMEOUT, "a kernel's bounded wait ran out (status 0x%08x)", word);

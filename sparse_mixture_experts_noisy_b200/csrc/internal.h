@@ -9,6 +9,17 @@ namespace moe {
 
 constexpr int kMaxExperts = 256;
 
+// Reads the status word at `at` on the device and clears it, synchronising s.  A
+// word of zero is left alone: a report that another stream's kernel makes between
+// the read and the clear would be lost with it.
+inline cudaError_t status_read_clear(uint32_t *at, uint32_t *word, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyAsync(word, at, sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *word == 0u) return e;
+    e = cudaMemsetAsync(at, 0, sizeof(uint32_t), s);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Launch with programmatic dependent launch allowed: the kernel may be

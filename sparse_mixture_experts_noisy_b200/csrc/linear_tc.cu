@@ -39,12 +39,9 @@ cudaError_t linear_status_address(uint32_t **word) {
 }
 
 cudaError_t linear_status_read_clear(uint32_t *word, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    static const uint32_t zero = 0u;
-    e = cudaMemcpyToSymbolAsync(g_linear_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(s);
+    uint32_t *at = nullptr;
+    cudaError_t e = linear_status_address(&at);
+    return e != cudaSuccess ? e : status_read_clear(at, word, s);
 }
 
 namespace {

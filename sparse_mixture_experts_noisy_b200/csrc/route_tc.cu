@@ -912,13 +912,9 @@ cudaError_t launch_route_tc(const void *x, const float *W_g, const float *b_g, c
 }
 
 cudaError_t route_status_read_clear(uint32_t *word, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_route_status_scratch, sizeof(uint32_t), 0,
-                                              cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    const uint32_t zero = 0u;
-    e = cudaMemcpyToSymbolAsync(g_route_status_scratch, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(s);
+    void *at = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&at, g_route_status_scratch);
+    return e != cudaSuccess ? e : status_read_clear(static_cast<uint32_t *>(at), word, s);
 }
 
 }  // namespace moe

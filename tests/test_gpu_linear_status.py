@@ -53,3 +53,17 @@ def test_refusals():
     for us in (0, 2000001):
         with pytest.raises(moe.MoeError, match="timeout_us"):
             moe.debug_linear_wait_timeout(us)
+
+
+def test_reports_made_while_another_stream_reads():
+    """Reads on one stream while reports arrive from another: each is found by one of the reads."""
+    require_gpu()
+    assert moe.check_linear_status() == (0, 0)
+    side = torch.cuda.Stream()
+    for _ in range(50):
+        moe.debug_linear_wait_timeout(200, stream=side)
+        done, found = False, 0
+        while not done:
+            done = side.query()          # asked first: the last read comes after the report
+            found += moe.check_linear_status()[0] == TIMEOUT
+        assert found == 1
