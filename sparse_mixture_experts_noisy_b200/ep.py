@@ -110,6 +110,7 @@ def _pad128(n: int) -> int:
     return max(128, (n + 127) // 128 * 128)
 
 
+@moe._on_stream
 def step_route(x, W_g, k, E, b_g=None, noise=None, sigma=0.0, stream=None):
     """Steps 1-2 (local part): routing and this rank's [k, E] counts."""
     topk, gates, _ = moe.moe_route(x, W_g, k, b_g=b_g, noise=noise, sigma=sigma, want_logits=False,
@@ -119,6 +120,7 @@ def step_route(x, W_g, k, E, b_g=None, noise=None, sigma=0.0, stream=None):
     return dict(topk=topk, gates=gates, ws=ws, counts_je=counts_je)
 
 
+@moe._on_stream
 def step_dispatch(st, x, E, k, cf, N_total, all_counts, rank, stream=None):
     """Steps 2-3: slots against the whole batch's capacity, expert-major rows."""
     base = moe.moe_shard_base(all_counts, rank, stream=stream)
@@ -141,6 +143,7 @@ def step_recv_buffers(plan: Plan, d: int, dtype, device):
     return bufs, [b[:n] for b, n in zip(bufs, plan.recv_splits)]
 
 
+@moe._on_stream
 def step_experts(plan: Plan, recv_bufs, W_up_local, W_down_local, stream=None, act=moe.ACT_RELU, b_up=None,
                  b_down=None):
     """Step 6: this rank's experts on each source's rows (one call per source)."""
@@ -170,6 +173,7 @@ def step_combine(st, stream=None):
     return moe.moe_combine(st["out_gathered"], d["slot"], st["topk"], d["offsets"], st["gates"], stream=stream)
 
 
+@moe._on_stream
 def expert_parallel_forward(x, W_g, W_up_local, W_down_local, k, cf, N_total, comm: Comm | None = None,
                             b_g=None, noise=None, sigma=0.0, stream=None):
     """This rank's part of one batch of N_total tokens with the experts split

@@ -702,7 +702,7 @@ class MoELayer:
     def __call__(self, x, noise=None, y=None, stream=None):
         if self._ws is None or x.shape[0] != self._ws_tokens:
             self._reserve(x.shape[0], x.dtype)
-        if torch.cuda.is_current_stream_capturing() and not any(w is self._ws for w in self._captured):
+        if x.is_cuda and torch.cuda.is_current_stream_capturing() and not any(w is self._ws for w in self._captured):
             self._captured.append(self._ws)
         return moe_forward(x, self.W_g, self.W_up, self.W_down, self.k, self.cf, b_g=self.b_g,
                            noise=noise, sigma=self.sigma, y=y, ws=self._ws, stream=stream, act=self.act,

@@ -36,6 +36,7 @@ def exchange_counts(counts_je: torch.Tensor, group=None) -> torch.Tensor:
     return torch.stack(parts)
 
 
+@moe._on_stream
 def sharded_forward(x, W_g, W_up, W_down, k, cf, N_total, group=None, b_g=None, noise=None, sigma=0.0,
                     stream=None):
     """This rank's part of one batch of N_total tokens.  x: [N_local, d] (device).

@@ -103,3 +103,40 @@ def test_the_layer(calls):
     layer = moe.MoELayer(a[1], a[2], a[3], K, None)
     layer(a[0], stream="side")
     assert seen and all(d >= 1 for _, d in seen) and all(d >= 1 for d in allocated)
+
+
+class OneRank:
+    def __init__(self, seen):
+        self.seen = seen
+
+    def world(self):
+        return 1
+
+    def rank(self):
+        return 0
+
+    def all_gather(self, t):
+        self.seen.append(("all_gather", Switch.depth))
+        return torch.zeros_like(t).unsqueeze(0)
+
+    def all_to_all(self, out, given):
+        self.seen.append(("all_to_all", Switch.depth))
+
+
+def test_collectives_follow_the_kernels(calls, monkeypatch):
+    """The exchanges read what the kernels wrote: they belong on the same stream."""
+    from sparse_mixture_experts_noisy_b200 import ep, shard
+    seen, allocated = calls
+    monkeypatch.setattr(moe, "_cuda", lambda t, name: None)   # what torch.empty gives here is on the host
+    x, Wg, up, dn, _, _ = arguments()["moe_forward"]
+    ep.expert_parallel_forward(x, Wg, up, dn, K, None, N, comm=OneRank(seen), stream="side")
+    names = {n for n, _ in seen}
+    assert {"all_gather", "all_to_all", "moe_shard_dispatch", "moe_combine"} <= names
+    assert all(d >= 1 for _, d in seen) and all(d >= 1 for d in allocated)
+    seen.clear(), allocated.clear()
+    monkeypatch.setattr(shard.dist, "get_rank", lambda group: 0)
+    monkeypatch.setattr(shard, "exchange_counts", lambda t, group: OneRank(seen).all_gather(t))
+    shard.sharded_forward(x, Wg, up, dn, K, None, N, stream="side")
+    assert "all_gather" in {n for n, _ in seen}
+    assert all(d >= 1 for _, d in seen) and all(d >= 1 for d in allocated)
+    assert Switch.depth == 0
