@@ -802,16 +802,17 @@ class GraphedForward:
         self.x = x
         self.noise = noise
         self.y = torch.empty_like(x)
-        layer._reserve(x.shape[0], x.dtype)
-        side = torch.cuda.Stream(device=x.device)
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
-            layer(x, noise=noise, y=self.y)   # first call outside the capture
-        torch.cuda.current_stream().wait_stream(side)
-        torch.cuda.synchronize(x.device)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
-            layer(x, noise=noise, y=self.y)
+        with torch.cuda.device(x.device):   # a capture is on the current device
+            layer._reserve(x.shape[0], x.dtype)
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                layer(x, noise=noise, y=self.y)   # first call outside the capture
+            torch.cuda.current_stream().wait_stream(side)
+            torch.cuda.synchronize()
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph, stream=side):
+                layer(x, noise=noise, y=self.y)
 
     def replay(self):
         self.graph.replay()
@@ -850,7 +851,7 @@ class HostPipeline:
     def submit(self, x_h, y_h, noise_h=None):
         b = self.i & 1
         g = self.graphs[b]
-        comp = torch.cuda.current_stream()
+        comp = torch.cuda.current_stream(g.x.device)
         with torch.cuda.stream(self.s_in):
             if self.used[b]:
                 self.s_in.wait_event(self.done[b])   # the forward of batch i-2 has read these inputs

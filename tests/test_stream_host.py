@@ -140,3 +140,40 @@ def test_collectives_follow_the_kernels(calls, monkeypatch):
     assert "all_gather" in {n for n, _ in seen}
     assert all(d >= 1 for _, d in seen) and all(d >= 1 for d in allocated)
     assert Switch.depth == 0
+
+
+def test_a_capture_is_on_the_inputs_device(calls, monkeypatch):
+    """GraphedForward switches to its input's device for the warm-up and the capture."""
+    inside = []
+
+    class On:
+        def __init__(self, device=None):
+            self.device = device
+
+        def __enter__(self):
+            inside.append(self)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+        def wait_stream(self, other):
+            assert inside
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: seen.append(bool(inside)) or On())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: seen.append(bool(inside)) or On())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: On())
+    monkeypatch.setattr(torch.cuda, "graph", lambda g, stream: On())
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", On)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
+
+    class Layer:
+        def _reserve(self, n, dtype):
+            seen.append(bool(inside))
+
+        def __call__(self, x, noise=None, y=None):
+            seen.append(len(inside) >= 2)   # the device, then the stream or the capture
+
+    moe.GraphedForward(Layer(), fake(N, D))
+    assert len(seen) == 6 and all(seen) and not inside
