@@ -98,10 +98,10 @@ linear_pack_kernel(const T *__restrict__ in0, int64_t rows0, __nv_bfloat16 *out0
 // the column sums of the unrounded dZ over a chunk of rows.  The rounding is what
 // the tensor cores take in bf16: dx and dW then have an error of 0.0024 of their
 // norm, 0.0017 with dZ in fp32 (32768 x 2048 -> 1408), and the experts' backward
-// rounds its dZ the same way.  In fp32 all bits of dZ go on, as three parts.  A block takes 256
-// columns, eight to a lane, its 8 warps every eighth row of the chunk, ROWS at a
-// time.  operand (rows of ld, fp32 in parts), plain (rows of n in the storage
-// type, for the CUDA-core products) and part are nullable.
+// rounds its dZ the same way.  In fp32 all bits of dZ go on, as three parts.
+// A block takes 256 columns, eight to a lane, its 8 warps every eighth row of the
+// chunk, ROWS at a time.  operand (rows of ld, fp32 in parts), plain (rows of n in
+// the storage type, for the CUDA-core products) and part are nullable.
 template <typename T>
 __global__ void __launch_bounds__(256, 2)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int64_t M, int n, int ld,
@@ -226,9 +226,9 @@ cudaError_t pack(const void *&in0, int64_t rows0, void *out0, const void *&in1, 
 // A few tokens: the CUDA-core kernels, unless W is an operand as it is, which
 // streams as fast through the tensor cores.  For fp32 they save a copy of W in
 // parts, 2.5 times its bytes: 16 x 4096 -> 4096 40.6 us with W from HBM and 30.0
-// with W in the L2 cache, 17 tokens through the tensor cores 43.1 and 42.9.  Padding a bf16 W costs less: 16 x 2281 -> 8176 39 and 23 us, 4 tokens 15
-// and 22; while W is small the saved launch counts more (16 x 301 -> 705 3.8 and
-// 7.0 us).
+// with W in the L2 cache; 17 tokens, through the tensor cores, 43.1 and 42.9.
+// Padding a bf16 W costs less: 16 x 2281 -> 8176 39 and 23 us, 4 tokens 15 and 22;
+// while W is small the saved launch counts more (16 x 301 -> 705 3.8 and 7.0 us).
 bool use_skinny(int64_t M, int dt, int cols, int other) {
     if (!needs_pack(dt, cols) || M > kSkinnyRows) return false;
     return dt == 0 || M <= 4 || static_cast<int64_t>(cols) * other <= (1 << 20);

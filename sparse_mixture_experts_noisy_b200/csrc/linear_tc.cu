@@ -622,7 +622,8 @@ template <typename T, int BN> constexpr int split_smem(int stage_bytes) {
 // this one whatever the call needs: it belongs to the kernel, and a call that set
 // a smaller one would take it from under another thread's launch.
 template <typename T, int BN> constexpr int split_smem_limit() {
-    constexpr int k = split_smem<T, BN>(split_stage_bytes<T, BN>(false)), mn = split_smem<T, BN>(split_stage_bytes<T, BN>(true));
+    constexpr int k = split_smem<T, BN>(split_stage_bytes<T, BN>(false));
+    constexpr int mn = split_smem<T, BN>(split_stage_bytes<T, BN>(true));
     static_assert(tmem_room(split_tmem_cols<BN>(), k < mn ? k : mn), "tensor memory");
     return k > mn ? k : mn;
 }
@@ -1075,7 +1076,8 @@ cudaError_t launch_split(const TcProduct *t, int count, int S, uint64_t timeout_
     a.timeout_ns = wait_limit(timeout_ns, t, count, SPLIT);
     const int smem = split_smem<T, BN>(stage_bytes);
     auto kern = linear_split_kernel<T, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem_limit<T, BN>());
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem_limit<T, BN>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));

@@ -89,3 +89,56 @@ def test_both_outputs_of_a_norm_in_place(d, dtype):
         got = moe.moe_layer_norm(c["x"], t["gamma"], t["beta"], residual=c["res"], y=c[y], sum_out=c[s])
         assert got[0] is c[y] and got[1] is c[s]
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@DTYPES
+def test_block_without_rows(dtype):
+    """An empty batch: empty outputs, zero gradients of the weights."""
+    require_gpu()
+    d, E, f = 64, 4, 128
+    r = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    layer = moe.MoELayer(r(E, d), r(E, f, d).to(dtype), r(E, d, f).to(dtype), 2, 1.25)
+    block = moe.MoEBlock(layer, shared=(r(96, d).to(dtype), r(96), r(d, 96).to(dtype), None))
+    x = torch.empty(0, d, device="cuda", dtype=dtype)
+    assert [o.shape for o in block(x, x)] == [(0, d), (0, d)]
+    s, m, saved = block.train(x, x)
+    assert s.shape == m.shape == (0, d)
+    g = block.backward(x, x, saved)
+    assert g.pop("dx").shape == (0, d)
+    assert len(g) == 10 and not any(bool(v.any()) for v in g.values())
+
+
+@DTYPES
+def test_blocks_on_two_streams(dtype):
+    """Two blocks with layers of their own, forward and backward on two streams at
+    once and joined by events, give the bits of one after the other."""
+    require_gpu()
+    d, E, f, n = 256, 8, 320, 500
+
+    def make(seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        layer = moe.MoELayer(r(E, d) / 16, (r(E, f, d) / 16).to(dtype), (r(E, d, f) / 18).to(dtype), 2, 1.25)
+        shared = ((r(384, d) / 16).to(dtype), r(384), (r(d, 384) / 20).to(dtype), r(d))
+        return moe.MoEBlock(layer, shared=shared, shared_act=moe.ACT_GELU), r(n, d).to(dtype), r(n, d).to(dtype)
+
+    def run(block, x, ds):
+        s, m, saved = block.train(x, x)
+        g = block.backward(ds, ds, saved)
+        return [s, m, *(g[q] for q in sorted(g))]
+
+    sets = [make(1), make(2)]
+    want = [run(*t) for t in sets]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(10):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(run(*sets[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for out in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
+    assert moe.check_linear_status() == (0, 0)
