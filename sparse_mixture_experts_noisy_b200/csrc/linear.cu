@@ -4,6 +4,7 @@
 //   dZ = dy act'(z),  dx = dZ W,  dW = dZ^T x,  db = sum over rows of dZ
 // This file holds the passes around the products (operands for the tensor cores,
 // dZ, db) and the host-side choice between the products' kernels.
+#include "colsum.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "linear.cuh"
@@ -163,28 +164,6 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, int act, int
         for (int w = 0; w < 8; ++w) s += red[w][threadIdx.x & 7][threadIdx.x >> 3];
         part[static_cast<int64_t>(blockIdx.y) * n + col] = s;
     }
-}
-
-// db = the chunks' sums added: 32 columns per block, each of 32 warps every 32nd
-// chunk, then a tree over the warps.
-__global__ void __launch_bounds__(1024)
-linear_db_kernel(const float *part, int64_t groups, int n, float *db) {
-    __shared__ float red[32][33];
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
-    float a = 0.0f;
-    if (col < n) {
-#pragma unroll 4
-        for (int64_t g = warp; g < groups; g += 32) a += part[g * n + col];
-    }
-    red[warp][lane] = a;
-    __syncthreads();
-    a = red[lane][warp];  // warp w now sums column w
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (lane == 0 && blockIdx.x * 32 + warp < n) db[blockIdx.x * 32 + warp] = a;
 }
 
 // Chunks of rows of the dZ pass: about four blocks an SM, at least 32 rows each.
@@ -360,8 +339,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs &a, void *ws, uint64_t timeout
             if (e != cudaSuccess) return e;
         }
         if (part != nullptr && chunks > 1) {
-            e = launch_pdl(linear_db_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(a.d_out) + 31) / 32)),
-                           dim3(1024), 0, s, part, chunks, a.d_out, a.db);
+            e = launch_col_reduce(part, chunks, a.d_out, 1, a.db, nullptr, s);
             if (e != cudaSuccess) return e;
         }
         if (!products) return e;

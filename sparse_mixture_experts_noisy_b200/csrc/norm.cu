@@ -11,6 +11,7 @@
 // Statistics, row sums and column sums are fp32; each output is rounded once.
 // The mean is taken first and the variance from the centred values, so a row
 // with a large common offset loses nothing.
+#include "colsum.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -141,31 +142,6 @@ norm_bwd_cols_kernel(const T *__restrict__ dy, const T *__restrict__ h, const fl
         p[col] = a;
         p[d + col] = b;
     }
-}
-
-// dgamma[c] = sum over g of part[g][0][c], dbeta[c] of part[g][1][c]: 32
-// columns per block, each of 32 warps every 32nd partial row, then a tree over
-// the warps.  out0/out1 nullable.
-__global__ void __launch_bounds__(1024)
-col_reduce_kernel(const float *part, int64_t groups, int d, float *out0, float *out1) {
-    __shared__ float red[32][33];
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
-    float *out = blockIdx.y == 0 ? out0 : out1;
-    if (out == nullptr) return;
-    float a = 0.0f;
-    if (col < d) {
-#pragma unroll 4
-        for (int64_t g = warp; g < groups; g += 32) a += part[(2 * g + blockIdx.y) * d + col];
-    }
-    red[warp][lane] = a;
-    __syncthreads();
-    a = red[lane][warp];  // warp w now sums column w
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = a;
 }
 
 // ---------------------------------------------------------------- rows held in registers
@@ -823,7 +799,7 @@ cudaError_t launch_norm_bwd(const void *dy, const void *h, int dt, const float *
     };
     cudaError_t e = dt == 1 ? go(__nv_bfloat16{}) : go(float{});
     if (e != cudaSuccess || !sums) return e;
-    return launch_pdl(col_reduce_kernel, dim3(cols, 2), dim3(1024), 0, s, part, rows, d, dgamma, dbeta);
+    return launch_col_reduce(part, rows, d, 2, dgamma, dbeta, s);
 }
 
 }  // namespace moe
